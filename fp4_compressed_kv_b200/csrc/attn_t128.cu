@@ -53,6 +53,7 @@
 #include <cuda_fp16.h>
 #include <mutex>
 
+#include "attn_common.cuh"
 #include "kvc_internal.cuh"
 #include "tc05_common.cuh"
 
@@ -79,77 +80,6 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t S_COL = 0, L_COL = 64, O_COL = 256;  // S^T, L^T: 64 cols; O^T: 4 x 64
 constexpr float kRescaleSlack = 8.0f;                // log2 units
 enum { BAR_S = 0, BAR_O = 1, BAR_Q = 2, BAR_W = 3 };
-
-// ---- TMA and bulk copies (non-multicast, into this CTA's shared memory)
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::
-            "r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-// The query tile of a record CTA, landed by TMA as bf16, converted in place to
-// f16 with a per-head power of two that puts the row maximum in [2^14,
-// 2^15); the head's softmax multiplier qs[h] absorbs it.  Thread t: head t/4,
-// channels [144 (t%4), +144) as 18 16-byte pieces (the same swizzled
-// positions the TMA wrote; a warp's accesses take the minimum 4 wavefronts).
-__device__ __forceinline__ void convert_q_f16(const AttnArgs& a, float sm_log2, uint32_t sQ,
-                                              uint32_t q_atom, float* qs, int tid) {
-    const int h = tid >> 2, qq = tid & 3;
-    uint4 v[18];
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-        const int c16 = 18 * qq + i;
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                     : "r"(sQ + (c16 >> 3) * q_atom + swz(h, c16 & 7)));
-    }
-    uint32_t amax = 0;  // max |x| as fp32 bits (integer order = float order)
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            amax = max(amax, (w[k] << 16) & 0x7FFFFFFFu);
-            amax = max(amax, w[k] & 0x7FFF0000u);
-        }
-    }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    int k = 0;
-    if (amax >= 0x7F800000u) {
-        if (qq == 0) set_status(a.status, KVC_DEV_NONFINITE);
-    } else if (amax != 0) {
-        const int e = (int)(amax >> 23) - 127;  // floor(log2 amax) for normal values
-        k = min(max(e - 14, -60), 113);
-    }
-    const float mul = __uint_as_float((uint32_t)(127 - k) << 23);
-    if (qq == 0) qs[h] = sm_log2 * __uint_as_float((uint32_t)(127 + k) << 23);
-#pragma unroll
-    for (int i = 0; i < 18; ++i) {
-        const int c16 = 18 * qq + i;
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            o[j] = pack_f16(__uint_as_float(w[j] << 16) * mul,
-                            __uint_as_float(w[j] & 0xFFFF0000u) * mul);
-        sts128(sQ + (c16 >> 3) * q_atom + swz(h, c16 & 7), o[0], o[1], o[2], o[3]);
-    }
-}
 
 // Scale byte index of 8-channel piece (item i, word u) for groups of G:
 // latent items 0..15, RoPE items 16..17 (groups restart at channel 512).
@@ -364,7 +294,7 @@ attn_t128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (!win && c0 < c1) {
         const bool got = warp == 0 ? mbar_wait(bQ, 0, wait_ns) : true;
         ok = __syncthreads_and(got) != 0;
-        if (ok && tid < 4 * HG) convert_q_f16(a, sm_log2, sQ, q_atom, qs, tid);
+        if (ok && tid < 4 * HG) convert_q_f16(a.status, sm_log2, sQ, q_atom, qs, tid);
     }
 
     for (int c = c0; c < c1 && ok; ++c) {
@@ -971,9 +901,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     });
     return fn;
 }
+}  // namespace
 // 2-D bf16 tensor [rows][576] (row stride 1152 B), boxes of 64 channels x
 // box_rows rows, 128-byte swizzle, zero fill past the end.
-bool encode_rows(CUtensorMap* m, const void* base, unsigned long long rows, unsigned box_rows) {
+bool encode_rows576(CUtensorMap* m, const void* base, unsigned long long rows, unsigned box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dims[2] = {(cuuint64_t)t128::D, (cuuint64_t)rows};
@@ -984,7 +915,6 @@ bool encode_rows(CUtensorMap* m, const void* base, unsigned long long rows, unsi
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-}  // namespace
 unsigned long long device_wait_limit_ns() { return g_wait_ns; }
 void set_device_wait_limit_ns(unsigned long long ns) { g_wait_ns = ns; }
 
@@ -1107,11 +1037,11 @@ static int launch_t128_g(const kvc_config& c, const AttnArgs& a, const Shape& sh
     // every CTA's query rows arrive by TMA (boxes of HG rows); so do bf16
     // window rows (boxes of a chunk, or of WR rows when folded)
     CUtensorMap tq = {}, tw = {}, twr = {};
-    if (!encode_rows(&tq, a.q, (unsigned long long)a.batch * t128::H, HG)) return -1;
+    if (!encode_rows576(&tq, a.q, (unsigned long long)a.batch * t128::H, HG)) return -1;
     if (wc > 0 && !a.win_fp8 &&
-        !encode_rows(&tw, a.window, (unsigned long long)a.batch * a.window_stride, t128::CK))
+        !encode_rows576(&tw, a.window, (unsigned long long)a.batch * a.window_stride, t128::CK))
         return -1;
-    if (WR && !encode_rows(&twr, a.window, (unsigned long long)a.batch * a.window_stride, WR))
+    if (WR && !encode_rows576(&twr, a.window, (unsigned long long)a.batch * a.window_stride, WR))
         return -1;
     const float sm_log2 = c.sm_scale * 1.4426950408889634f;
     trace_before("attn_t128", s);

@@ -637,6 +637,198 @@ kvc_status kvc_index_topk_batched(const kvc_config* cfg, int nq, const int8_t* i
                : KVC_ERR_CUDA;
 }
 
+kvc_status kvc_norm_rope(const kvc_config* cfg, int n_rows, const void* q, int64_t q_stride,
+                         const float* q_gain, int q_norm, void* q_out, const void* k,
+                         int64_t k_stride, const float* k_gain, int k_norm, void* k_out,
+                         const int32_t* positions, const float* inv_freq, float eps, int layout,
+                         uint32_t* dev_status, void* stream) {
+    const NvtxRange nvtx_range("kvc_norm_rope");
+    Shape sh;
+    if (!derive_shape(cfg, &sh)) return KVC_ERR_INVALID;
+    if (n_rows < 0 || !(eps >= 0.f) || !(eps < 1e30f)) return KVC_ERR_INVALID;
+    if (layout != KVC_ROPE_HALVES && layout != KVC_ROPE_PAIRS) return KVC_ERR_INVALID;
+    for (int norm : {q_norm, k_norm})
+        if (norm != KVC_NORM_NONE && norm != KVC_NORM_LATENT && norm != KVC_NORM_ROW)
+            return KVC_ERR_INVALID;
+    if (n_rows == 0) return KVC_OK;
+    if (!q && !k) return KVC_ERR_INVALID;
+    if ((q && !q_out) || (k && !k_out) || !positions || (sh.D > sh.Dv && !inv_freq))
+        return KVC_ERR_INVALID;
+    const int64_t q_row = (int64_t)cfg->n_heads * sh.D;
+    if (q && (q_stride < q_row || q_stride > ((int64_t)1 << 40) || q_stride * sh.act_bytes % 16 ||
+              !aligned(q, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16)))
+        return KVC_ERR_INVALID;
+    if (k && (k_stride < sh.D || k_stride > ((int64_t)1 << 40) || k_stride * sh.act_bytes % 16 ||
+              !aligned(k, 16) || !aligned(k_out, 16) || !aligned(k_gain, 16)))
+        return KVC_ERR_INVALID;
+    // rows may be rotated in place only where input and output rows coincide
+    if ((q && q == q_out && q_stride != q_row) || (k && k == k_out && k_stride != sh.D))
+        return KVC_ERR_INVALID;
+    if (!aligned(positions, 4) || !aligned(inv_freq, 4)) return KVC_ERR_INVALID;
+    if ((int64_t)n_rows * (cfg->n_heads + 1) > ((int64_t)1 << 34)) return KVC_ERR_CAPACITY;
+    if (!device_ok()) return KVC_ERR_DEVICE;
+    const auto width = [&](int norm) {
+        return norm == KVC_NORM_ROW ? sh.D : norm == KVC_NORM_LATENT ? sh.Dv : 0;
+    };
+    NormRopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_gain = q_gain;
+    a.k_gain = k_gain;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.n_rows = n_rows;
+    a.q_heads = q ? cfg->n_heads : 0;
+    a.D = sh.D;
+    a.latent = sh.Dv;
+    a.rope = sh.D - sh.Dv;
+    a.q_width = width(q_norm);
+    a.k_width = width(k_norm);
+    a.pairs = layout == KVC_ROPE_PAIRS;
+    a.eps = eps;
+    a.status = dev_status;
+    return launch_norm_rope(*cfg, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_unpack(const kvc_config* cfg, const kvc_cache* cache, const int32_t* idx, int first,
+                      int n, void* rows, uint32_t* dev_status, void* stream) {
+    const NvtxRange nvtx_range("kvc_unpack");
+    Shape sh;
+    if (!derive_shape(cfg, &sh)) return KVC_ERR_INVALID;
+    if (!cache || !cache->records || !cache->n_entries) return KVC_ERR_INVALID;
+    if (cache->batch < 0 || cache->capacity < 0) return KVC_ERR_INVALID;
+    if (cache->batch > 65535) return KVC_ERR_CAPACITY;  // batch is a grid dimension
+    if (!aligned(cache->records, 16) || !aligned(cache->n_entries, 4)) return KVC_ERR_INVALID;
+    if (n < 0 || (!idx && (first < 0 || (int64_t)first + n > cache->capacity)))
+        return KVC_ERR_INVALID;
+    if (n == 0 || cache->batch == 0) return KVC_OK;
+    if (!rows || !aligned(rows, 16) || !aligned(idx, 4)) return KVC_ERR_INVALID;
+    if (!device_ok()) return KVC_ERR_DEVICE;
+    UnpackArgs a = {};
+    a.records = static_cast<const uint8_t*>(cache->records);
+    a.n_entries = cache->n_entries;
+    a.idx = idx;
+    a.first = idx ? 0 : first;
+    a.n = n;
+    a.batch = cache->batch;
+    a.capacity = cache->capacity;
+    a.out = rows;
+    a.status = dev_status;
+    return launch_unpack(*cfg, sh, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_unpack_window_fp8(const kvc_config* cfg, const uint8_t* codes, const float* scales,
+                                 int64_t n_rows, void* rows, void* stream) {
+    const NvtxRange nvtx_range("kvc_unpack_window_fp8");
+    Shape sh;
+    if (!derive_shape(cfg, &sh)) return KVC_ERR_INVALID;
+    if (n_rows < 0 || n_rows > ((int64_t)1 << 40)) return KVC_ERR_INVALID;
+    if (n_rows == 0) return KVC_OK;
+    if (!codes || !scales || !rows) return KVC_ERR_INVALID;
+    if (!aligned(rows, 16) || !aligned(codes, 8) || !aligned(scales, 4)) return KVC_ERR_INVALID;
+    if (!device_ok()) return KVC_ERR_DEVICE;
+    return launch_unpack_fp8(*cfg, sh, codes, scales, n_rows, rows,
+                             static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_tree_decode_attn(const kvc_config* cfg, int n_nodes, const void* q,
+                                const kvc_cache* cache, const int32_t* topk_idx, int topk_shared,
+                                const void* window, int window_len, const int32_t* window_lens,
+                                const void* draft, const int32_t* parents, void* out, float* lse,
+                                uint32_t* dev_status, void* stream) {
+    const NvtxRange nvtx_range("kvc_tree_decode_attn");
+    Shape sh;
+    if (!derive_shape(cfg, &sh)) return KVC_ERR_INVALID;
+    if (!cache || !cache->records || !cache->n_entries) return KVC_ERR_INVALID;
+    if (cache->batch < 0 || cache->capacity < 0) return KVC_ERR_INVALID;
+    if (cache->batch > 65535) return KVC_ERR_CAPACITY;
+    if (!aligned(cache->records, 16) || !aligned(cache->n_entries, 4)) return KVC_ERR_INVALID;
+    if ((int64_t)cache->capacity * sh.rb > ((int64_t)1 << 40)) return KVC_ERR_CAPACITY;
+    if (n_nodes < 0 || (topk_shared != 0 && topk_shared != 1)) return KVC_ERR_INVALID;
+    if (n_nodes > kMaxTreeNodes) return KVC_ERR_CAPACITY;
+    if (window_len < 0 || window_len > cfg->window) return KVC_ERR_INVALID;
+    if (n_nodes == 0 || cache->batch == 0) return KVC_OK;
+    if (!q || !topk_idx || !draft || !parents || !out || (window_len > 0 && !window))
+        return KVC_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(draft, 16) || !aligned(out, 16) || !aligned(topk_idx, 4) ||
+        !aligned(parents, 4) || !aligned(window, 16) || !aligned(window_lens, 4) ||
+        !aligned(lse, 4))
+        return KVC_ERR_INVALID;
+    if (!device_ok()) return KVC_ERR_DEVICE;
+    TreeArgs a = {};
+    a.q = q;
+    a.records = static_cast<const uint8_t*>(cache->records);
+    a.n_entries = cache->n_entries;
+    a.topk_idx = topk_idx;
+    a.topk_shared = topk_shared;
+    a.window = window;
+    a.window_len = window_len;
+    a.window_stride = cfg->window;
+    a.window_lens = window_lens;
+    a.draft = draft;
+    a.parents = parents;
+    a.out = out;
+    a.lse = lse;
+    a.status = dev_status;
+    a.nodes = n_nodes;
+    a.batch = cache->batch;
+    a.capacity = cache->capacity;
+    return launch_tree(*cfg, sh, a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KVC_OK
+               : KVC_ERR_CUDA;
+}
+
+kvc_status kvc_verify_tree(int batch, int n_nodes, int vocab, int dtype, const void* p,
+                           int64_t p_stride, const void* q, int64_t q_stride,
+                           const int32_t* tokens, const int32_t* parents, const float* u,
+                           const float* v, int32_t* path, int32_t* n_path, int32_t* next_token,
+                           uint32_t* dev_status, void* stream) {
+    const NvtxRange nvtx_range("kvc_verify_tree");
+    if (batch < 0 || n_nodes < 1 || vocab < 1 || (dtype != KVC_F32 && dtype != KVC_BF16))
+        return KVC_ERR_INVALID;
+    if (n_nodes > kMaxTreeNodes || vocab > kMaxVocab || batch > 65535) return KVC_ERR_CAPACITY;
+    if (batch == 0) return KVC_OK;
+    const int size = dtype == KVC_BF16 ? 2 : 4;
+    const int64_t most = (int64_t)1 << 40;
+    if (!p || !tokens || !parents || !u || !v || !path || !n_path || !next_token)
+        return KVC_ERR_INVALID;
+    if (p_stride < vocab || p_stride > most || (q && (q_stride < vocab || q_stride > most)))
+        return KVC_ERR_INVALID;
+    if (!aligned(p, size) || !aligned(q, size) || !aligned(tokens, 4) || !aligned(parents, 4) ||
+        !aligned(u, 4) || !aligned(v, 4) || !aligned(path, 4) || !aligned(n_path, 4) ||
+        !aligned(next_token, 4))
+        return KVC_ERR_INVALID;
+    if (!device_ok()) return KVC_ERR_DEVICE;
+    VerifyArgs a = {};
+    a.p = p;
+    a.q = q;
+    a.p_ld = p_stride;
+    a.q_ld = q ? q_stride : 0;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.u = u;
+    a.v = v;
+    a.path = path;
+    a.n_path = n_path;
+    a.next = next_token;
+    a.status = dev_status;
+    a.batch = batch;
+    a.nodes = n_nodes;
+    a.vocab = vocab;
+    return launch_verify(a, dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KVC_OK
+                                                                                    : KVC_ERR_CUDA;
+}
+
 kvc_status kvc_e2m1_encode(const float* x, int64_t n, uint8_t* codes, void* stream) {
     const NvtxRange nvtx_range("kvc_e2m1_encode");
     if (n < 0 || (n > 0 && (!x || !codes))) return KVC_ERR_INVALID;

@@ -187,6 +187,79 @@ cudaError_t launch_attention(const kvc_config& c, const Shape& sh, const AttnArg
 cudaError_t launch_window_fp8(const kvc_config& c, const Shape& sh, const void* rows, long long n,
                               uint8_t* codes, float* scales, uint32_t* status, cudaStream_t s);
 
+// Norms and position rotation of query rows [n_rows][q_heads][D] and key rows
+// [n_rows][D] (either may be absent: null, or q_heads = 0).  Strides between
+// rows of tokens in elements; outputs contiguous.  width = leading channels
+// under the norm (0, latent or D).
+struct NormRopeArgs {
+    const void* q;
+    const void* k;
+    void* q_out;
+    void* k_out;
+    long long q_stride, k_stride;
+    const float* q_gain;     // [q_width] or null
+    const float* k_gain;     // [k_width] or null
+    const int32_t* positions;  // [n_rows]
+    const float* inv_freq;     // [rope / 2]
+    int n_rows, q_heads, D, latent, rope, q_width, k_width, pairs;
+    float eps;
+    uint32_t* status;
+};
+cudaError_t launch_norm_rope(const kvc_config& c, const NormRopeArgs& a, cudaStream_t s);
+
+// Records read back as rows [batch][n][D] of act_dtype.
+struct UnpackArgs {
+    const uint8_t* records;
+    const int32_t* n_entries;
+    const int32_t* idx;  // [batch][n], or null: entries first .. first + n - 1
+    int first, n, batch, capacity;
+    void* out;
+    uint32_t* status;
+};
+cudaError_t launch_unpack(const kvc_config& c, const Shape& sh, const UnpackArgs& a,
+                          cudaStream_t s);
+// FP8 window rows [n][D] codes with a scale a row, read back as act_dtype.
+cudaError_t launch_unpack_fp8(const kvc_config& c, const Shape& sh, const uint8_t* codes,
+                              const float* scales, long long n, void* rows, cudaStream_t s);
+
+// Attention of a tree of drafted tokens (node-major arrays: node t of
+// sequence b is row t * batch + b).
+constexpr int kMaxTreeNodes = 256;
+struct TreeArgs {
+    const void* q;           // [T][B][H][D]
+    const uint8_t* records;  // [B][cap][rb]
+    const int32_t* n_entries;
+    const int32_t* topk_idx;    // [T][B][K], or [B][K] when shared
+    const void* window;         // [B][W][D]
+    const int32_t* window_lens; // [B] or null
+    const void* draft;          // [T][B][D]
+    const int32_t* parents;     // [T][B]
+    void* out;                  // [T][B][H][Dv] act_dtype
+    float* lse;                 // [T][B][H] or null
+    uint32_t* status;
+    int nodes, batch, capacity, topk_shared, window_len, window_stride;
+};
+cudaError_t launch_tree(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s);
+
+// Verification of drafted trees: rows of p and q (null: drafts taken as
+// certain) are p_ld / q_ld elements apart, node t of sequence b row t * batch + b.
+constexpr int kMaxVocab = 1 << 22;
+struct VerifyArgs {
+    const void* p;
+    const void* q;
+    long long p_ld, q_ld;
+    const int32_t* tokens;   // [T][B]
+    const int32_t* parents;  // [T][B]
+    const float* u;          // [T][B]
+    const float* v;          // [B]
+    int32_t* path;           // [B][T]
+    int32_t* n_path;         // [B]
+    int32_t* next;           // [B]
+    uint32_t* status;
+    int batch, nodes, vocab;
+};
+cudaError_t launch_verify(const VerifyArgs& a, int dtype, cudaStream_t s);
+
 cudaError_t launch_fp4_codec(const float* x, int64_t n, uint8_t* out, int e4m3,
                              cudaStream_t s);
 

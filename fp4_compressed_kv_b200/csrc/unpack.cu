@@ -1,0 +1,145 @@
+// unpack.cu -- packed records and FP8 window rows read back as rows of
+// values.
+//
+// Method: "DeepSeek V1 到 V4.1-Flash，单 token 的 global KV 如何从 389,000 B
+// 压缩到 890 B的？" (acejoy.com) part 4 "P4 main KV" (an element is stored
+// relative to its group's scale and multiplied back on use; the window stays
+// in FP8).  v_c = E2M1(code_c) * scale_group(c), or E4M3(code_c) * scale_row.
+//
+// A record is read once (a quarter of what a bf16 row takes) and its row
+// written once: the bound is HBM, and four fifths of its bytes are writes.  A
+// thread turns 8 channels (4 code bytes) into one 16-byte store (two for
+// fp32), so a warp's stores cover 512 contiguous bytes; its products are one
+// conversion and one multiplication a channel.  Products of a code (two
+// significant bits) and a UE4M3 scale (four) are exact in bf16; with fp32
+// scales they are rounded to fp32 and then to the row's type.
+#include <algorithm>
+#include <cuda_fp16.h>
+
+#include "kvc_internal.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int NT = 256;
+
+// Eight E2M1 codes (channel 2i in the low nibble of byte i) times a scale.
+__device__ __forceinline__ void e2m1x8_values(uint32_t codes, float scale, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(codes));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+        v[2 * k] = f.x * scale;
+        v[2 * k + 1] = f.y * scale;
+    }
+}
+__device__ __forceinline__ void put8(__nv_bfloat16* dst, const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[k]) : "f"(v[2 * k + 1]), "f"(v[2 * k]));
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void put8(float* dst, const float (&v)[8]) {
+    reinterpret_cast<float4*>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Grid (tiles of rows, batch); a block takes `rows` consecutive output rows.
+template <typename T, bool UE4M3>
+__global__ void __launch_bounds__(NT)
+unpack_kernel(UnpackArgs a, Shape sh, int rows) {
+    // (no early launch of dependents: kvc_pack reads its tokens before it waits
+    // for the kernel in front of it, and these rows may be its tokens)
+    pdl_wait();
+    const int b = blockIdx.y, np = sh.D >> 3, np_lat = sh.Dv >> 3;
+    const int n = a.n_entries[b];
+    const bool len_ok = n >= 0 && n <= a.capacity;
+    if (!len_ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, KVC_DEV_BAD_LENGTH);
+    const int j0 = blockIdx.x * rows, nj = min(rows, a.n - j0);
+    const uint8_t* base = a.records + (size_t)b * a.capacity * sh.rb;
+    T* out = static_cast<T*>(a.out) + ((size_t)b * a.n + j0) * sh.D;
+    const int lat_groups = (sh.Dv + sh.G - 1) / sh.G;
+    const int lg = 31 - __clz(sh.lpg);  // 8-channel pieces of a group: a power of two
+    for (int p = threadIdx.x; p < nj * np; p += NT) {
+        const int j = p / np, c = p - j * np;
+        int e = a.idx ? __ldg(a.idx + (size_t)b * a.n + j0 + j) : a.first + j0 + j;
+        if (e < 0 || e >= n || !len_ok) {
+            if (a.idx && e != -1 && len_ok && c == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
+            e = -1;
+        }
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (e >= 0) {
+            const uint8_t* rec = base + (size_t)e * sh.rb;
+            const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(rec) + c);
+            const int g = c < np_lat ? c >> lg : lat_groups + ((c - np_lat) >> lg);
+            const float scale =
+                UE4M3 ? e4m3_to_f32(__ldg(rec + sh.code_bytes + g))
+                      : __ldg(reinterpret_cast<const float*>(rec + sh.code_bytes) + g);
+            e2m1x8_values(codes, scale, v);
+        }
+        put8(out + (size_t)p * 8, v);
+    }
+}
+
+// FP8 window rows: thread = 8 channels of a row.
+template <typename T>
+__global__ void __launch_bounds__(NT)
+unpack_fp8_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales, long long n,
+                  int np, T* __restrict__ rows) {
+    pdl_wait();
+    for (long long p = (long long)blockIdx.x * NT + threadIdx.x; p < n * np;
+         p += (long long)gridDim.x * NT) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(codes) + p);
+        const float s = __ldg(scales + p / np);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = e4m3s_to_f32(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 0xFFu) * s;
+        put8(rows + p * 8, v);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_unpack(const kvc_config& c, const Shape& sh, const UnpackArgs& a,
+                          cudaStream_t s) {
+    const int rows = 16;
+    const dim3 grid((a.n + rows - 1) / rows, a.batch);
+    const bool u = c.scale_fmt == KVC_SCALE_UE4M3;
+    trace_before("unpack", s);
+    cudaError_t e;
+    if (c.act_dtype == KVC_BF16)
+        e = u ? launch_pdl(unpack_kernel<__nv_bfloat16, true>, grid, NT, 0, s, a, sh, rows)
+              : launch_pdl(unpack_kernel<__nv_bfloat16, false>, grid, NT, 0, s, a, sh, rows);
+    else
+        e = u ? launch_pdl(unpack_kernel<float, true>, grid, NT, 0, s, a, sh, rows)
+              : launch_pdl(unpack_kernel<float, false>, grid, NT, 0, s, a, sh, rows);
+    trace_after(s);
+    return e;
+}
+
+cudaError_t launch_unpack_fp8(const kvc_config& c, const Shape& sh, const uint8_t* codes,
+                              const float* scales, long long n, void* rows, cudaStream_t s) {
+    const int np = sh.D / 8;
+    const unsigned grid = (unsigned)std::min<long long>((n * np + NT - 1) / NT, 148 * 64);
+    trace_before("unpack_fp8", s);
+    const cudaError_t e =
+        c.act_dtype == KVC_BF16
+            ? launch_pdl(unpack_fp8_kernel<__nv_bfloat16>, grid, NT, 0, s, codes, scales, n, np,
+                         static_cast<__nv_bfloat16*>(rows))
+            : launch_pdl(unpack_fp8_kernel<float>, grid, NT, 0, s, codes, scales, n, np,
+                         static_cast<float*>(rows));
+    trace_after(s);
+    return e;
+}
+
+}  // namespace kvc

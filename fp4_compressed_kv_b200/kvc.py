@@ -21,6 +21,8 @@ STATUS_NAMES = {0: "ok", 1: "invalid", 2: "capacity", 3: "cuda", 4: "unsupported
 SCALE_F32, SCALE_UE4M3 = 0, 1
 FULL, REINDEX, REUSE = 0, 1, 2
 F32, BF16 = 0, 1
+NORM_NONE, NORM_LATENT, NORM_ROW = 0, 1, 2
+ROPE_HALVES, ROPE_PAIRS = 0, 1
 DEV_NONFINITE, DEV_BAD_INDEX, DEV_CAPACITY, DEV_TIMEOUT, DEV_BAD_LENGTH = 1, 2, 4, 8, 16
 
 
@@ -71,6 +73,13 @@ def _lib():
             "kvc_index_topk_batched": (S, [P, I, P, P, P, P, Z, P, P]),
             "kvc_layer_group_step_hier": (S, [P, I, I, I, P, P, P, P, I, P, P, P, P, P, Z, P,
                                               P]),
+            "kvc_unpack": (S, [P, P, P, I, I, P, P, P]),
+            "kvc_unpack_window_fp8": (S, [P, P, P, C.c_int64, P, P]),
+            "kvc_norm_rope": (S, [P, I, P, C.c_int64, P, I, P, P, C.c_int64, P, I, P, P, P,
+                                  C.c_float, I, P, P]),
+            "kvc_tree_decode_attn": (S, [P, I, P, P, P, I, P, I, P, P, P, P, P, P, P]),
+            "kvc_verify_tree": (S, [I, I, I, I, P, C.c_int64, P, C.c_int64, P, P, P, P, P, P, P,
+                                    P, P]),
             "kvc_e2m1_encode": (S, [P, C.c_int64, P, P]),
             "kvc_e4m3_encode": (S, [P, C.c_int64, P, P]),
             "kvc_trace_begin": (S, [I]),
@@ -112,6 +121,29 @@ def _ptr(t):
 def _stream(stream):
     s = stream if stream is not None else torch.cuda.current_stream()
     return C.c_void_p(s.cuda_stream)
+
+
+def _operand(name, t, dtype, shape, contiguous=True):
+    """Device address of an operand (None stays None), checked: type, shape,
+    contiguity, and that it lives on the current device (the library's work
+    and pointers belong to it)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current CUDA device")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _act(cfg: Config):
+    return torch.bfloat16 if cfg.act_dtype == BF16 else torch.float32
+
+
+def _status(status):
+    return None if status is None else _operand("status", status, torch.int32, (1,))
 
 
 def make_config(latent_dim, rope_dim, group, scale_fmt, idx_dim, topk, window, n_heads, sm_scale,
@@ -161,6 +193,20 @@ class Cache:
             self.idx_k = torch.zeros(batch, capacity, cfg.idx_dim, dtype=torch.int8,
                                      device=device)
         self.n_entries = torch.zeros(batch, dtype=torch.int32, device=device)
+
+    @classmethod
+    def wrap(cls, cfg: Config, records, idx_k, n_entries):
+        """A cache over buffers the caller already has: records [B][cap][record
+        bytes] uint8, idx_k [B][cap][indexer row bytes], n_entries [B] int32."""
+        self = cls.__new__(cls)
+        self.cfg, (self.batch, self.capacity) = cfg, records.shape[:2]
+        self.records, self.idx_k, self.n_entries = records, idx_k, n_entries
+        lead = (self.batch, self.capacity)
+        _operand("records", records, torch.uint8, (*lead, record_bytes(cfg)))
+        _operand("idx_k", idx_k, torch.uint8 if cfg.idx_fmt == 1 else torch.int8,
+                 (*lead, idx_row_bytes(cfg)))
+        _operand("n_entries", n_entries, torch.int32, (self.batch,))
+        return self
 
     def struct(self) -> CacheStruct:
         return CacheStruct(self.records.data_ptr(), self.idx_k.data_ptr(),
@@ -272,6 +318,109 @@ def layer_group_step(cfg, modes, q, idx_q, windows, window_len, cache: Cache, ou
     _check("kvc_layer_group_step", _lib().kvc_layer_group_step(
         C.byref(cfg), len(modes), modes_arr, _ptr(q), _ptr(idx_q), _ptr(windows), int(window_len),
         C.byref(cs), _ptr(out), _ptr(lse), _ptr(topk), p, n, _ptr(status), _stream(stream)))
+
+
+def unpack(cfg, cache: Cache, rows, idx=None, first=0, status=None, stream=None):
+    """Records read back: rows [B][n][D] act_dtype receives entries idx [B][n]
+    int32 (-1: zeros), or entries first .. first + n - 1 without idx."""
+    n = rows.shape[1]
+    d = cfg.latent_dim + cfg.rope_dim
+    cs = cache.struct()
+    _check("kvc_unpack", _lib().kvc_unpack(
+        C.byref(cfg), C.byref(cs), _operand("idx", idx, torch.int32, (cache.batch, n)), int(first),
+        n, _operand("rows", rows, _act(cfg), (cache.batch, n, d)), _status(status),
+        _stream(stream)))
+
+
+def unpack_window_fp8(cfg, codes, scales, rows, stream=None):
+    """codes [..][D] uint8 (signed E4M3) and scales [..] fp32, as
+    pack_window_fp8 writes them -> rows [..][D] act_dtype."""
+    d = cfg.latent_dim + cfg.rope_dim
+    lead = scales.shape
+    _check("kvc_unpack_window_fp8", _lib().kvc_unpack_window_fp8(
+        C.byref(cfg), _operand("codes", codes, torch.uint8, (*lead, d)),
+        _operand("scales", scales, torch.float32, lead), scales.numel(),
+        _operand("rows", rows, _act(cfg), (*lead, d)), _stream(stream)))
+
+
+def norm_rope(cfg, q, k, positions, inv_freq, q_out, k_out, q_gain=None, k_gain=None,
+              q_norm=NORM_ROW, k_norm=NORM_LATENT, eps=1e-6, layout=ROPE_HALVES, status=None,
+              stream=None):
+    """Norms and position rotation of query rows q [n][H][D] and key rows k
+    [n][D] (either may be None, with its output); their first dimension may be
+    strided (a slice of a wider projection), the outputs are contiguous."""
+    n, h, d = positions.shape[0], cfg.n_heads, cfg.latent_dim + cfg.rope_dim
+    act = _act(cfg)
+    width = (0, cfg.latent_dim, d)
+    qs = ks = 0
+    if q is not None:
+        qs = q.stride(0) if n > 1 else h * d
+        if q.stride(2) != 1 or (h > 1 and q.stride(1) != d):
+            raise ValueError("q: the heads of a token must be contiguous")
+        if q_out is None:
+            raise ValueError("q_out: needed with q")
+    if k is not None:
+        ks = k.stride(0) if n > 1 else d
+        if k.stride(1) != 1:
+            raise ValueError("k: the channels of a row must be contiguous")
+        if k_out is None:
+            raise ValueError("k_out: needed with k")
+    _check("kvc_norm_rope", _lib().kvc_norm_rope(
+        C.byref(cfg), n, _operand("q", q, act, (n, h, d), False), qs,
+        _operand("q_gain", q_gain, torch.float32, (width[q_norm],)), q_norm,
+        _operand("q_out", q_out, act, (n, h, d)) if q is not None else None,
+        _operand("k", k, act, (n, d), False), ks,
+        _operand("k_gain", k_gain, torch.float32, (width[k_norm],)), k_norm,
+        _operand("k_out", k_out, act, (n, d)) if k is not None else None,
+        _operand("positions", positions, torch.int32, (n,)),
+        _operand("inv_freq", inv_freq, torch.float32, (cfg.rope_dim // 2,)), float(eps), layout,
+        _status(status), _stream(stream)))
+
+
+def tree_decode_attn(cfg, q, cache: Cache, topk, window, window_len, draft, parents, out, lse=None,
+                     window_lens=None, status=None, stream=None):
+    """Attention of T drafted tokens per sequence, each over its selected
+    entries and the window of its own path: q [T][B][H][D], topk [T][B][K] or
+    [B][K] (one selection for all nodes), window [B][W][D], draft [T][B][D],
+    parents [T][B] -> out [T][B][H][latent] act_dtype."""
+    t, b, d = q.shape[0], cache.batch, cfg.latent_dim + cfg.rope_dim
+    act, h, shared = _act(cfg), cfg.n_heads, topk.dim() == 2
+    cs = cache.struct()
+    _check("kvc_tree_decode_attn", _lib().kvc_tree_decode_attn(
+        C.byref(cfg), t, _operand("q", q, act, (t, b, h, d)), C.byref(cs),
+        _operand("topk", topk, torch.int32, (b, cfg.topk) if shared else (t, b, cfg.topk)),
+        int(shared), _operand("window", window, act, (b, cfg.window, d)), int(window_len),
+        _operand("window_lens", window_lens, torch.int32, (b,)),
+        _operand("draft", draft, act, (t, b, d)),
+        _operand("parents", parents, torch.int32, (t, b)),
+        _operand("out", out, act, (t, b, h, cfg.latent_dim)),
+        _operand("lse", lse, torch.float32, (t, b, h)), _status(status), _stream(stream)))
+
+
+def verify_tree(p, q, tokens, parents, u, v, path, n_path, next_token, status=None, stream=None):
+    """Verify drafted trees: target and draft probabilities p, q [T][B][V]
+    (fp32 or bf16; q None: greedy drafts; rows may be padded to equal steps),
+    tokens, parents, u [T][B], v [B] -> path [B][T], n_path [B], next_token [B]."""
+    t, b, vocab = p.shape
+
+    def rows(name, x):  # equally spaced rows t * B + b of contiguous entries
+        step = x.stride(1) if b > 1 else x.stride(0) if t > 1 else vocab
+        if (x.stride(2) != 1 and vocab > 1) or (t > 1 and b > 1 and x.stride(0) != b * step):
+            raise ValueError(f"{name}: rows must be contiguous and equally spaced")
+        return _operand(name, x, p.dtype, (t, b, vocab), False), step
+
+    if p.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("p: expected fp32 or bf16 probabilities")
+    pp, ps = rows("p", p)
+    qp, qs = rows("q", q) if q is not None else (None, 0)
+    _check("kvc_verify_tree", _lib().kvc_verify_tree(
+        b, t, vocab, F32 if p.dtype == torch.float32 else BF16, pp, ps, qp, qs,
+        _operand("tokens", tokens, torch.int32, (t, b)),
+        _operand("parents", parents, torch.int32, (t, b)),
+        _operand("u", u, torch.float32, (t, b)), _operand("v", v, torch.float32, (b,)),
+        _operand("path", path, torch.int32, (b, t)),
+        _operand("n_path", n_path, torch.int32, (b,)),
+        _operand("next_token", next_token, torch.int32, (b,)), _status(status), _stream(stream)))
 
 
 def e2m1_encode(x, codes, stream=None):

@@ -63,6 +63,8 @@ typedef enum {
 typedef enum { KVC_SCALE_F32 = 0, KVC_SCALE_UE4M3 = 1 } kvc_scale_fmt;
 typedef enum { KVC_FULL = 0, KVC_REINDEX = 1, KVC_REUSE = 2 } kvc_mode;
 typedef enum { KVC_F32 = 0, KVC_BF16 = 1 } kvc_dtype;
+typedef enum { KVC_NORM_NONE = 0, KVC_NORM_LATENT = 1, KVC_NORM_ROW = 2 } kvc_norm;
+typedef enum { KVC_ROPE_HALVES = 0, KVC_ROPE_PAIRS = 1 } kvc_rope_layout;
 
 /* device status bits */
 #define KVC_DEV_NONFINITE 0x1u  /* a NaN/Inf input: a pack channel (coded as 0)
@@ -70,7 +72,8 @@ typedef enum { KVC_F32 = 0, KVC_BF16 = 1 } kvc_dtype;
 #define KVC_DEV_BAD_INDEX 0x2u  /* a top-K index outside [-1, n_entries)       */
 #define KVC_DEV_CAPACITY 0x4u   /* pack would pass the cache capacity          */
 #define KVC_DEV_TIMEOUT 0x8u    /* a bounded in-kernel wait gave up            */
-#define KVC_DEV_BAD_LENGTH 0x10u /* n_entries outside [0, capacity]            */
+#define KVC_DEV_BAD_LENGTH 0x10u /* n_entries outside [0, capacity], or a window
+                                    length outside [0, window_len]             */
 
 /* Shape and format of one compressed cache and its decode attention.
  *  latent_dim  Dv, latent channels; also the value width ([A] breakthrough 2: 512)
@@ -272,6 +275,134 @@ kvc_status kvc_sparse_decode_attn_fp8win(const kvc_config* cfg, const void* q,
                                          size_t ws_bytes, uint32_t* dev_status,
                                          void* stream);
 
+/* Records read back as rows ([A] part 4 "P4 main KV": an element is stored
+ * relative to its group's scale and multiplied back on use).
+ * rows [batch][n][D] act_dtype receives E2M1(code) x scale of every channel,
+ * rounded once to act_dtype (bf16 rows of UE4M3 scales are exact; with fp32
+ * scales the fp32 product is rounded).
+ * idx  [batch][n] int32 entries to read, in any order and repeated as wanted
+ *      (a kvc_index_topk output fits), or NULL for entries first .. first+n-1
+ *      of every sequence (first >= 0, first + n <= capacity; `first` is not
+ *      read when idx is given).
+ * A row without a stored entry is written as zeros: index -1, an entry at or
+ * past n_entries[b] (silently without idx; with idx it sets
+ * KVC_DEV_BAD_INDEX), every row of a sequence whose n_entries is outside
+ * [0, capacity] (KVC_DEV_BAD_LENGTH).  cache->idx_k is not used and may be
+ * NULL.                                                                     */
+kvc_status kvc_unpack(const kvc_config* cfg, const kvc_cache* cache,
+                      const int32_t* idx, int first, int n, void* rows,
+                      uint32_t* dev_status, void* stream);
+
+/* FP8 window rows read back: codes [n_rows][D] and scales [n_rows] as
+ * kvc_pack_window_fp8 writes them -> rows [n_rows][D] act_dtype, the fp32
+ * product E4M3(code) x scale rounded to act_dtype.  codes 8-byte, rows
+ * 16-byte aligned.                                                          */
+kvc_status kvc_unpack_window_fp8(const kvc_config* cfg, const uint8_t* codes,
+                                 const float* scales, int64_t n_rows,
+                                 void* rows, void* stream);
+
+/* RMS norms of query and key rows for each head and the rotation of their
+ * RoPE channels by position, in one pass: the rows that kvc_pack, the windows
+ * and the attention take.
+ * q    [n_rows][n_heads][D] act_dtype queries, or NULL for none; a token's
+ *      heads are contiguous, tokens are q_stride elements apart (at least
+ *      n_heads D), so q may be a slice of a wider matrix.  q_out
+ *      [n_rows][n_heads][D] is contiguous.
+ * k    [n_rows][D] act_dtype key rows, or NULL for none, k_stride elements
+ *      apart (at least D); k_out [n_rows][D] is contiguous.
+ * norm (q_norm, k_norm, a kvc_norm): the channels under the norm, none, the
+ *      latent_dim first ones, or all D.  y_c = x_c / sqrt(mean x^2 + eps) g_c
+ *      over them, others pass.  gain (q_gain, k_gain): g, one fp32 per channel
+ *      under the norm, 16-byte aligned, or NULL for ones.
+ * positions [n_rows] int32; inv_freq [rope_dim/2] fp32 (may be NULL without
+ *      RoPE channels).  Pair i of the RoPE channels is turned by positions[r]
+ *      x inv_freq[i] radians after the norm: channels (i, i + rope_dim/2)
+ *      (KVC_ROPE_HALVES) or (2i, 2i + 1) (KVC_ROPE_PAIRS).  The angle is
+ *      formed and reduced in fp64, so far positions keep their precision.
+ * Sums and products are fp32, rounded once to act_dtype.  Row starts 16-byte
+ * aligned (base pointers and strides).  A row whose sum of squares is not
+ * finite in fp32 sets KVC_DEV_NONFINITE (its output is what the formula
+ * gives).  In place (q_out = q, k_out = k) where the stride is the contiguous
+ * one; other overlaps of inputs and outputs are not allowed.               */
+kvc_status kvc_norm_rope(const kvc_config* cfg, int n_rows, const void* q,
+                         int64_t q_stride, const float* q_gain, int q_norm,
+                         void* q_out, const void* k, int64_t k_stride,
+                         const float* k_gain, int k_norm, void* k_out,
+                         const int32_t* positions, const float* inv_freq,
+                         float eps, int layout, uint32_t* dev_status,
+                         void* stream);
+
+/* Attention of a tree of drafted tokens ([A] breakthrough 2 and 4): what
+ * kvc_sparse_decode_attn computes, for n_nodes drafted tokens of every
+ * sequence in one launch, each behind its own ancestors.  Arrays over nodes
+ * are node-major, as kvc_index_topk_batched's queries are.
+ * q        [n_nodes][batch][n_heads][D] act_dtype queries.
+ * topk_idx [n_nodes][batch][topk] selected entries of each node, or
+ *          [batch][topk], one selection for all nodes of a sequence, when
+ *          topk_shared = 1; -1 entries are skipped, any other index outside
+ *          [0, n_entries[b]) is skipped and sets KVC_DEV_BAD_INDEX.
+ * window   [batch][window][D] act_dtype raw keys of the tokens in front of
+ *          the tree, oldest first; the first window_len rows of sequence b are
+ *          used, or the first window_lens[b] of them when window_lens [batch]
+ *          (device) is given (outside [0, window_len]: taken as 0,
+ *          KVC_DEV_BAD_LENGTH).
+ * draft    [n_nodes][batch][D] act_dtype raw keys of the drafted tokens.
+ * parents  [n_nodes][batch] int32: the parent of node t, below t; -1 for a
+ *          node that follows the window directly, -2 for no node there.  Any
+ *          other value sets KVC_DEV_BAD_INDEX and counts as -2, as does a node
+ *          under such a one.
+ * A node's raw keys are the last cfg->window tokens of its own path: the
+ * window rows, then the draft rows from its first ancestor down to itself.
+ * One softmax runs jointly over them and its selected entries.
+ * out      [n_nodes][batch][n_heads][latent_dim] act_dtype; lse
+ *          [n_nodes][batch][n_heads] fp32 or NULL.  With no key at all, and
+ *          where there is no node, the output row is 0 and lse is -inf.
+ * n_nodes <= 256 (else KVC_ERR_CAPACITY).  n_entries outside [0, capacity]
+ * sets KVC_DEV_BAD_LENGTH; the sequence's entries are then skipped.
+ * cache->idx_k is not used and may be NULL.  No workspace.                  */
+kvc_status kvc_tree_decode_attn(const kvc_config* cfg, int n_nodes, const void* q,
+                                const kvc_cache* cache, const int32_t* topk_idx,
+                                int topk_shared, const void* window,
+                                int window_len, const int32_t* window_lens,
+                                const void* draft, const int32_t* parents,
+                                void* out, float* lse, uint32_t* dev_status,
+                                void* stream);
+
+/* Verification of drafted trees against the target's probabilities, from
+ * given random numbers; the accepted tokens and the next one are distributed
+ * as the target's.
+ * Node 0 of every sequence is the root: a token already accepted (the last
+ * one sampled).  parents as in kvc_tree_decode_attn; nodes that are not below
+ * the root are never reached, and parents[0][b] = -2 means that sequence b has
+ * no tree (n_path 0, next_token -1).
+ * p        row t * batch + b, p_stride elements apart (at least vocab): the
+ *          target's probabilities of the token behind node t of sequence b;
+ *          fp32 or bf16 (dtype, a kvc_dtype).
+ * q        the same for the draft's probabilities that the children of node t
+ *          were drawn from, independently; or NULL: every child was chosen for
+ *          certain (greedy drafts), siblings with different tokens.
+ * tokens   [n_nodes][batch] drafted tokens (node 0's is not read); outside
+ *          [0, vocab): the node is left out, KVC_DEV_BAD_INDEX.
+ * u        [n_nodes][batch], v [batch] fp32 random numbers in [0, 1).
+ * The children of the last accepted node are tried in order of index, r = its
+ * row of p and m = 1 at first: token x is accepted where u m q(x) < r(x);
+ * otherwise r becomes max(r - m q, 0) and m its sum (with q NULL: accepted
+ * where u m < r(x), otherwise r(x) leaves r and m).  A residual without mass
+ * ends the tries and gives way to the row of p.  next_token is the lowest i
+ * with r(0) + ... + r(i) > v sum r.  All of it in fp64; probabilities that are
+ * negative or not finite count as 0 (the latter set KVC_DEV_NONFINITE).
+ * path     [batch][n_nodes] int32: the accepted nodes from 0 on, -1 behind.
+ * n_path   [batch] their number; next_token [batch] (-1, KVC_DEV_NONFINITE,
+ *          when its row of p has no mass).
+ * n_nodes <= 256, vocab <= 4,194,304, batch <= 65,535 (else KVC_ERR_CAPACITY). */
+kvc_status kvc_verify_tree(int batch, int n_nodes, int vocab, int dtype,
+                           const void* p, int64_t p_stride, const void* q,
+                           int64_t q_stride, const int32_t* tokens,
+                           const int32_t* parents, const float* u,
+                           const float* v, int32_t* path, int32_t* n_path,
+                           int32_t* next_token, uint32_t* dev_status,
+                           void* stream);
+
 /* One decode step through a CSA2 layer group (A11; [A] part 4 "CSA2：三种模式，
  * 40 层只存 4 份"): layers run in order on `stream`.
  *  Full    -- indexer top-K with its own idx_q over `cache`, then attention;
@@ -332,7 +463,8 @@ kvc_status kvc_e4m3_encode(const float* x, int64_t n, uint8_t* bytes, void* stre
  * "pack", "pack_idx", "pack_commit", "window_fp8", "index_scan",
  * "index_scan_tc", "index_scan_fp4", "topk_select", "topk_select_fp4",
  * "block_max", "copy_topk", "attn_t128", "attn_simt", "attn_merge",
- * "fp4_codec".  Every enqueuing entry point also opens an NVTX range named
+ * "fp4_codec", "norm_rope", "unpack", "unpack_fp8", "tree_t128",
+ * "tree_simt", "verify".  Every enqueuing entry point also opens an NVTX range named
  * after itself for the duration of the call (a no-op without a profiler).  */
 kvc_status kvc_trace_begin(int max_launches);
 kvc_status kvc_trace_end(void);

@@ -213,7 +213,7 @@ cudaError_t launch_tree_simt(const kvc_config& c, const Shape& sh, const TreeArg
 }  // namespace
 
 cudaError_t launch_tree(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s) {
-    return launch_tree_simt(c, sh, a, s);
+    return tree_t128_supported(c, sh) ? launch_tree_t128(c, sh, a, s) : launch_tree_simt(c, sh, a, s);
 }
 
 }  // namespace kvc

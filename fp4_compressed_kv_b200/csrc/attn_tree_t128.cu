@@ -1,0 +1,942 @@
+// attn_tree_t128.cu -- attention of a tree of drafted tokens on the
+// 5th-generation tensor cores: 576-channel entries (512 latent + 64 RoPE),
+// bf16 queries, a multiple of 16 heads.
+//
+// Method: "DeepSeek V1 到 V4.1-Flash，单 token 的 global KV 如何从 389,000 B
+// 压缩到 890 B的？" (acejoy.com) part 3 breakthrough 2 and 4, as in attn_tree.cu
+// (the mathematics) and attn_t128.cu (the products: keys are the MMA's M
+// dimension, 128 keys against up to 64 heads; S^T = K Q^T and O^T += V^T P^T
+// in tensor memory).  What differs from the single-token kernel:
+//
+//  * A node's keys are its raw rows (window rows and the drafted rows of its
+//    path, gathered by 16-byte asynchronous copies) and then its records, in
+//    chunks of 128.  Raw chunks run with bf16 operands against the query rows
+//    as they landed; the query tile is then turned into f16 in place and the
+//    record chunks run in f16, where every dequantised entry is exact.  Both
+//    kinds add into the same fp32 accumulators.
+//  * One K tile of 147 KB is all that fits beside the queries, so overlap is
+//    made inside it: the latent channels are four pairs of 64-channel atoms,
+//    PV product mt is the only one that reads pair mt, and its commit frees
+//    the pair for the next chunk's values while the products mt + 1 ... run;
+//    QK of the next chunk starts on pair 0 as soon as that is filled.  Roles:
+//      warps 0-7   softmax (thread = key, half of the heads each) and output
+//      warps 8-15  loads: the next chunk's records are in registers (two
+//                  threads a key, 32 + 32 bytes a pair and half the RoPE
+//                  codes) while this one's are converted and stored
+//      warp 16     one thread issues the products and the queries' TMA
+//      warp 17     walks the next node's path through the parents
+//    so the tensor pipe waits only for the softmax of the chunk it works on.
+//  * With many nodes a CTA takes node after node (the next node's queries,
+//    path and records arrive while this one's last products run); with few,
+//    the CTAs of a cluster split one node's chunks, push their partial sums
+//    to the owners of the heads over distributed shared memory, and each
+//    owner joins its heads' rows in split order.
+//
+// Bound: the products' operand reads from shared memory (each of 68 products
+// a chunk reads 6 KB at 128 B a clock, 3.3 K clocks) and the softmax between
+// QK and PV of one chunk.
+//
+// Every wait on an mbarrier is bounded and no other barrier is used inside
+// the roles; on expiry a role sets KVC_DEV_TIMEOUT and leaves, the others
+// follow when their own waits expire, products and copies in flight get a last
+// bounded wait, the tensor memory is freed.
+#include <algorithm>
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+#include "kvc_internal.cuh"
+#include "tc05_common.cuh"
+
+namespace kvc {
+namespace tree {
+
+using namespace tc;
+
+constexpr int D = 576, DV = 512, CK = 128, NATOM = 9;
+constexpr int SOFT_WARPS = 8, LOAD_WARPS = 8, MMA_WARP = 16, PATH_WARP = 17;
+constexpr int NT = 20 * 32;  // (whole warpgroups: registers are shared out by them)
+constexpr uint32_t K_ATOM = CK * 128;  // 128 rows x 128 B
+constexpr uint32_t OFF_Q = 0;
+constexpr uint32_t OFF_K = NATOM * 64 * 128;            // 73,728
+constexpr uint32_t OFF_P = OFF_K + 8 * K_ATOM;          // the RoPE atom, P^T after QK
+constexpr uint32_t OFF_MISC = OFF_K + NATOM * K_ATOM;   // 221,184
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t S_COL = 0, O_COL = 256;
+// A head's reference is put kTop (log2 units) below its largest logit and moved
+// when one passes it by more than kMost: weights go up to 2^15, so that f16
+// still has full precision for those 2^-21 of the largest (2^-32 of it below).
+constexpr float kTop = 7.0f, kMost = 15.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Item {  // what the roles know of one node
+    int c0, c1;     // this CTA's chunks: raw ones below nraw, then records
+    int nraw;       // raw chunks
+    int raw, skip;  // raw keys, and older ones out of the window
+    int wl, depth, n;
+};
+
+struct Misc {
+    float qs[2][64];               // softmax multiplier of the f16 queries, by item parity
+    float wmax[2][2][4][32];       // chunk maxima: [chunk parity][head half][quadrant][head]
+    float2 sm[SOFT_WARPS][32];     // each softmax warp's (multiplier, -reference)
+    float fac[SOFT_WARPS][32];     // each softmax warp's rescale factors
+    float lsum[2][4][32];          // sums of weights: [head half][quadrant][head]
+    unsigned char valid[2][CK];    // keys of the chunk that count, by chunk parity
+    short parents[kMaxTreeNodes];  // path warp's
+    unsigned char up[2][kMaxTreeNodes];  // ancestors k steps up, by item parity
+    Item item[2];
+    uint64_t bars[24];
+    uint32_t tmem;
+    int failed;
+    float ml[72 * 2];              // exchange: (m, l) of [split][head]
+    float wts[72];                 // exchange: weights [head][split]
+    uint32_t row_at[64], ml_at[64];  // exchange: owners' addresses
+    float inv[64];
+};
+constexpr uint32_t SMEM_BYTES = OFF_MISC + sizeof(Misc) + 1024;  // + alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
+
+enum {
+    B_FULL = 0,   // [5] pair p (4: RoPE) of the chunk is in place (8 warps)
+    B_FREE = 5,   // [4] PV product mt is done (commit); the last covers all
+    B_S = 9,      // QK done (commit)
+    B_P = 10,     // P^T is in place (8 warps)
+    B_Q = 11,     // query rows landed (TMA)
+    B_Q16 = 12,   // queries in f16 (8 warps)
+    B_MAX = 13,   // [2] chunk maxima of a head half (4 warps)
+    B_INFO = 15,  // [2] item of that parity published
+    B_ITEM = 17,  // [2] item of that parity finished by everyone (17 warps)
+    B_SUM = 19,   // [2] sums of weights of a head half (4 warps)
+    B_END = 21,
+    N_BARS = 22
+};
+
+// A warpgroup's registers a thread.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[N]) {
+    if constexpr (N == 8) tmem_ld8(addr, r);
+    else if constexpr (N == 16) tmem_ld16(addr, r);
+    else tmem_ld32(addr, r);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
+    if constexpr (N == 32) {
+        tmem_st32(addr, r);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(
+                             addr + i),
+                         "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]),
+                         "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+                         : "memory");
+        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+    }
+}
+// 16 bytes to shared memory, asynchronously; zeros without a source row.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
+                 "r"(live ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+// Sums over a warp's lanes of N values each: lane l gets that of value l % N.
+template <int N>
+__device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
+#pragma unroll
+    for (int o = 16; o >= N; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+#pragma unroll
+    for (int o = N / 2; o >= 1; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const float send = lane & o ? v[i] : v[i + o], keep = lane & o ? v[i + o] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    return v[0];
+}
+
+// The query tile, landed by TMA as bf16, turned into f16 in place with a power
+// of two a head that puts the row's maximum in [2^14, 2^15); the head's softmax
+// multiplier qs[h] takes it back.  Thread t: head t / 4, channels [144 (t % 4),
+// + 144) as 18 pieces of 16 bytes, read twice (maximum, then conversion) rather
+// than held: the records of the next chunk are in registers meanwhile.
+__device__ __forceinline__ void queries_to_f16(uint32_t* status, float sm_log2, uint32_t sQ,
+                                               uint32_t q_atom, float* qs, int t) {
+    const int h = t >> 2, qq = t & 3;
+    auto piece = [&](int i) { return sQ + ((18 * qq + i) >> 3) * q_atom + swz(h, (18 * qq + i) & 7); };
+    auto load = [&](int i, uint32_t(&w)[4]) {
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(piece(i)));
+    };
+    uint32_t amax = 0;  // max |x| as fp32 bits (integer order = float order)
+#pragma unroll 6
+    for (int i = 0; i < 18; ++i) {
+        uint32_t w[4];
+        load(i, w);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+    }
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    int k = 0;
+    if (amax >= 0x7F800000u) {
+        if (qq == 0) set_status(status, KVC_DEV_NONFINITE);
+    } else if (amax != 0) {
+        k = min(max((int)(amax >> 23) - 127 - 14, -60), 113);  // floor(log2 amax) - 14
+    }
+    const float mul = __uint_as_float((uint32_t)(127 - k) << 23);
+    if (qq == 0) qs[h] = sm_log2 * __uint_as_float((uint32_t)(127 + k) << 23);
+#pragma unroll 6
+    for (int i = 0; i < 18; ++i) {
+        uint32_t w[4];
+        load(i, w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            w[j] = pack_f16(__uint_as_float(w[j] << 16) * mul,
+                            __uint_as_float(w[j] & 0xFFFF0000u) * mul);
+        sts128(piece(i), w[0], w[1], w[2], w[3]);
+    }
+}
+
+// A thread's part of a chunk: one key, and of each pair the 64 channels of one
+// atom (32 code bytes), of the RoPE atom 32 channels (16 code bytes).  Scale
+// words: those holding the scales of these channels.
+template <int G>
+struct Rec {
+    static constexpr int SW = G == 8 ? 2 : 1;
+    uint4 code[4][2];
+    uint32_t scale[4][SW];
+    uint4 rope;
+    uint32_t rope_scale;
+    __device__ __forceinline__ void load_pair(const uint8_t* rec, int p, int sub) {
+        code[p][0] = ldg_nc(rec + 64 * p + 32 * sub);
+        code[p][1] = ldg_nc(rec + 64 * p + 32 * sub + 16);
+        const uint32_t* sc = reinterpret_cast<const uint32_t*>(rec + 288);
+        const int first = (128 * p + 64 * sub) / G;  // scale byte of the first channel
+#pragma unroll
+        for (int i = 0; i < SW; ++i) scale[p][i] = __ldg(sc + (first >> 2) + i);
+    }
+    __device__ __forceinline__ void load_rope(const uint8_t* rec, int sub) {
+        rope = ldg_nc(rec + 256 + 16 * sub);
+        const int first = 512 / G + (32 * sub) / G;
+        rope_scale = __ldg(reinterpret_cast<const uint32_t*>(rec + 288) + (first >> 2));
+    }
+};
+
+// 32 channels (four words of codes) into 16-byte pieces c16 .. c16 + 3 of a
+// row; byte0 is the scale byte's place of the first channel in words.
+template <int G>
+__device__ __forceinline__ void store32(uint32_t row, int x7, int c16, const uint4& code,
+                                        const uint32_t* words, int byte0, bool live) {
+    const uint32_t c[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (live) {
+            const int sb = byte0 + (8 * k) / G;
+            const uint32_t word = G == 8 ? words[sb >> 2] : words[0];
+            e2m1x8_scaled(c[k], ue4m3_f16x2((word >> (8 * (sb & 3))) & 0xFFu), w);
+        }
+        sts128(row + (((uint32_t)(c16 + k) ^ x7) << 4), w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int G, int HG>
+__global__ void __launch_bounds__(NT, 1)
+tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, int H, int K,
+                 float sm_log2, int nsplit, unsigned long long wait_ns) {
+    constexpr int NH = HG / 2;                        // heads of a softmax warp
+    constexpr uint32_t Q_ATOM = (uint32_t)HG * 128u;  // packed atoms of HG rows
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    unsigned char* smem = smem_raw + (base - raw_base);
+    const uint32_t sQ = base + OFF_Q, sK = base + OFF_K, sP = base + OFF_P;
+    Misc& ms = *reinterpret_cast<Misc*>(smem + OFF_MISC);
+    const uint32_t bars = smem_u32(ms.bars);
+    auto bar = [&](int i) { return bars + 8u * i; };
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = blockIdx.x % nsplit;
+    const int first = blockIdx.x / nsplit, step = gridDim.x / nsplit;
+    const int nhg = H / HG, total = a.nodes * a.batch * nhg;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
+                         smem_u32(&ms.tmem)),
+                     "r"(TMEM_COLS));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    if (tid == 0) {
+        for (int i = 0; i < N_BARS; ++i) {
+            const int count = i < B_FREE || i == B_P || i == B_Q16 ? 8
+                              : i == B_MAX || i == B_MAX + 1 || i == B_SUM || i == B_SUM + 1 ? 4
+                              : i == B_ITEM || i == B_ITEM + 1     ? 17
+                                                                   : 1;
+            mbar_init(bar(i), count);
+        }
+        ms.failed = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    pdl_wait();
+
+    bool ok = true;
+    int gc = 0;  // chunks so far (phase of the chunk barriers)
+    int mine = 0;           // exchange: this CTA's chunks of its one item
+    float mref = -INFINITY, lv = 0.f;  // softmax warps: reference and sum of weights of head
+                                       // lane (of the warp's half)
+    // A whole warp's wait: its lanes leave with one answer.
+    auto warp_wait = [&](int i, int parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wait_ns)) != 0;
+    };
+    // The item's facts, once the path warp has published them.
+    auto get_item = [&](int it, Item& x) {
+        ok = warp_wait(B_INFO + (it & 1), (it >> 1) & 1);
+        if (ok) x = ms.item[it & 1];
+        return ok;
+    };
+
+    // Registers: 640 threads start with 96 each; while the roles run the last
+    // warpgroup gives up 40 a thread and the two of the softmax take 16 each
+    // (256 x 112 + 256 x 96 + 128 x 56 = 60,416 of 61,440).
+    if (warp < SOFT_WARPS) {
+        // ------------------------------------------------ softmax and output
+        more_registers<112>();
+        const int q = warp & 3, half = warp >> 2, hb = half * NH;
+        const int s = q * 32 + lane;  // key of a chunk, tensor-memory lane
+        const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16);
+        int it = 0, nsum = 0;
+        for (int w = first; w < total && ok; w += step, ++it) {
+            Item x;
+            if (!get_item(it, x)) break;
+            mref = -INFINITY;
+            lv = 0.f;
+            // sums of this thread's key's weights (fp32, unrounded), added
+            // over the lanes once at the end
+            float l[NH];
+#pragma unroll
+            for (int i = 0; i < NH; ++i) l[i] = 0.f;
+            for (int c = x.c0; c < x.c1; ++c, ++gc) {
+                const bool raw = c < x.nraw;
+                ok = warp_wait(B_S, gc & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const bool valid = ms.valid[gc & 1][s];
+                uint32_t r[NH];
+                tmem_ld<NH>(ta + S_COL + hb, r);
+                tmem_wait_ld();
+                // the chunk's maximum of every head: over the warp's keys, then
+                // over the four quadrants
+                float mx = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NH; ++i) {
+                    if (!valid) r[i] = 0xFF800000u;  // -inf
+                    const float m = warp_max(__uint_as_float(r[i]));
+                    if (lane == i) mx = m;
+                }
+                float(&wm)[4][32] = ms.wmax[gc & 1][half];
+                wm[q][lane] = mx;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_MAX + half));
+                ok = warp_wait(B_MAX + half, gc & 1);
+                if (!ok) break;
+                const float my = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
+                const float mul = raw || lane >= NH ? sm_log2 : ms.qs[it & 1][hb + lane];
+                const float mc = my * mul;
+                const float mo = mref;
+                const float mn = (mo == -INFINITY || mc > mo + kMost) ? mc - kTop : mo;
+                const float f = mo == -INFINITY ? 1.f : ex2(mo - mn);
+                mref = mn;
+                ms.sm[warp][lane] = make_float2(mul, mn == -INFINITY ? 0.f : -mn);
+                ms.fac[warp][lane] = f;
+                const bool moved = __any_sync(0xffffffffu, lane < NH && c > x.c0 && f != 1.f);
+                if (moved)
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) l[i] *= ms.fac[warp][i];
+                // weights 2^(x - reference) of the key, a 16-byte piece of 8 heads at a time
+#pragma unroll
+                for (int c8 = 0; c8 < NH / 8; ++c8) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int h = 8 * c8 + 2 * u;
+                        const float4 k = *reinterpret_cast<const float4*>(&ms.sm[warp][h]);
+                        const float p0 = ex2(fmaf(__uint_as_float(r[h]), k.x, k.y));
+                        const float p1 = ex2(fmaf(__uint_as_float(r[h + 1]), k.z, k.w));
+                        l[h] += p0;
+                        l[h + 1] += p1;
+                        v[u] = raw ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+                    }
+                    sts128(sP + swz(s, (hb >> 3) + c8), v[0], v[1], v[2], v[3]);
+                }
+                fence_async_smem();
+                if (moved) {
+                    // rare: a reference moved by more than the slack: what the
+                    // accumulators hold of the earlier chunks is rescaled
+                    ok = warp_wait(B_FREE + 3, (gc - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int t = 0; t < 4; ++t) {
+                        const uint32_t at = ta + O_COL + 64 * t + hb;
+                        uint32_t o[NH];
+                        tmem_ld<NH>(at, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < NH; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * ms.fac[warp][i]);
+                        tmem_st<NH>(at, o);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P));
+            }
+            if (!ok) break;
+            if (x.c1 > x.c0) {
+                float(&ls)[4][32] = ms.lsum[half];
+                ls[q][lane] = lane_sums<NH>(l, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SUM + half));
+                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 3, (gc - 1) & 1);
+                if (!ok) break;
+                lv = (ls[0][lane] + ls[1][lane]) + (ls[2][lane] + ls[3][lane]);
+                tc_fence_after();
+                mine = 1;
+            }
+            if (nsplit == 1) {
+                // ---- output: lane = channel of a tile; two lanes trade halves of
+                // two heads so that a lane stores two channels of one head
+                const int hg0 = (w % nhg) * HG, id = w / nhg;
+                const int b = id / a.nodes, t = id - b * a.nodes;
+                const size_t row = ((size_t)t * a.batch + b) * H + hg0 + hb;
+                if (q == 0 && a.lse && lane < NH)
+                    a.lse[row + lane] = lv == 0.f ? -INFINITY : (mref + __log2f(lv)) * kLn2;
+                ms.fac[warp][lane] = lv == 0.f ? 0.f : 1.f / lv;
+                __syncwarp();
+                __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + (row + (lane & 1)) * DV +
+                                     q * 32 + (lane & ~1);
+#pragma unroll 1
+                for (int mt = 0; mt < 4; ++mt) {
+                    uint32_t o[NH];
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) o[i] = 0u;
+                    if (x.c1 > x.c0) {
+                        tmem_ld<NH>(ta + O_COL + 64 * mt + hb, o);
+                        tmem_wait_ld();
+                    }
+#pragma unroll
+                    for (int i = 0; i < NH; i += 2) {
+                        const float2 k = *reinterpret_cast<const float2*>(&ms.fac[warp][i]);
+                        const float u = __uint_as_float(o[i]) * k.x;
+                        const float v = __uint_as_float(o[i + 1]) * k.y;
+                        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? u : v, 1);
+                        const uint32_t two = lane & 1 ? pack_bf16(got, v) : pack_bf16(u, got);
+                        *reinterpret_cast<uint32_t*>(out + (size_t)i * DV + mt * 128) = two;
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ITEM + (it & 1)));
+        }
+        fewer_registers<96>();
+    } else if (warp < SOFT_WARPS + LOAD_WARPS) {
+        // ------------------------------------------------------------- loads
+        const int lw = warp - SOFT_WARPS;
+        const int key = lw * 16 + (lane & 7) + ((lane >> 4) << 3), sub = (lane >> 3) & 1;
+        const uint32_t x7 = key & 7;
+        const uint32_t krow = sK + (uint32_t)sub * K_ATOM + (uint32_t)(key >> 3) * 1024u + x7 * 128u;
+        const uint32_t rrow = sK + 8 * K_ATOM + (uint32_t)(key >> 3) * 1024u + x7 * 128u;
+        auto filled = [&](int p) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_FULL + p));
+        };
+        int it = 0, nq = 0;
+        for (int w = first; w < total && ok; w += step, ++it) {
+            Item x;
+            if (!get_item(it, x)) break;
+            const int hg0 = (w % nhg) * HG, id = w / nhg;
+            const int b = id / a.nodes, t = id - b * a.nodes;
+            const int node = t * a.batch + b;
+            const int32_t* sel = a.topk_idx + (a.topk_shared ? (size_t)b : (size_t)node) * K;
+            const uint8_t* recs = a.records + (size_t)b * a.capacity * rb;
+            // record of this thread's key in chunk c, or -1
+            auto pick = [&](int c) {
+                const int j = (c - x.nraw) * CK + key;
+                if (j >= K || x.n < 0) return -1;
+                const int idx = __ldg(sel + j);
+                if (idx >= 0 && idx < x.n) return idx;
+                if (idx != -1 && sub == 0 && hg0 == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
+                return -1;
+            };
+            Rec<G> rec;
+            int cur = -1;
+            const int cr = max(x.c0, x.nraw);  // first record chunk
+            if (cr < x.c1) {
+                cur = pick(cr);
+                if (cur >= 0) {
+                    const uint8_t* src = recs + (size_t)cur * rb;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) rec.load_pair(src, p, sub);
+                    rec.load_rope(src, sub);
+                }
+            }
+            // ---- raw chunks
+            int c = x.c0;
+            for (; c < min(x.nraw, x.c1); ++c, ++gc) {
+                const int j = c * CK + key, r = x.skip + j;
+                const bool live = j < x.raw;
+                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.draft);
+                if (live)
+                    src = r < x.wl ? static_cast<const __nv_bfloat16*>(a.window) +
+                                         ((size_t)b * a.window_stride + r) * D
+                                   : src + ((size_t)ms.up[it & 1][x.depth - 1 - (r - x.wl)] * a.batch +
+                                            b) * D;
+#pragma unroll 1
+                for (int p = 0; p < 4 && ok; ++p) {
+                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        cp16(krow + (uint32_t)(2 * p) * K_ATOM + (((uint32_t)k ^ x7) << 4),
+                             src + (2 * p + sub) * 64 + 8 * k, live);
+                    cp_commit();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    cp16(rrow + (((uint32_t)(4 * sub + k) ^ x7) << 4), src + 512 + 32 * sub + 8 * k,
+                         live);
+                cp_commit();
+                if (sub == 0) ms.valid[gc & 1][key] = live;
+                cp_wait<4>();
+                filled(0);
+                cp_wait<3>();
+                filled(1);
+                cp_wait<2>();
+                filled(2);
+                cp_wait<1>();
+                filled(3);
+                cp_wait<0>();
+                filled(4);
+            }
+            if (!ok) break;
+            // ---- the queries to f16, once the raw chunks' products have read them
+            if (cr < x.c1) {
+                ok = warp_wait(B_Q, nq & 1);
+                if (ok && c > x.c0) ok = warp_wait(B_S, (gc - 1) & 1);
+                if (!ok) break;
+                const int ct = tid - SOFT_WARPS * 32;
+                if (ct < 4 * HG) queries_to_f16(a.status, sm_log2, sQ, Q_ATOM, ms.qs[it & 1], ct);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q16));
+            }
+            if (x.c1 > x.c0) ++nq;
+            // ---- record chunks
+            for (; c < x.c1; ++c, ++gc) {
+                const int next = c + 1 < x.c1 ? pick(c + 1) : -1;
+                const uint8_t* nsrc = recs + (size_t)(next < 0 ? 0 : next) * rb;
+                const bool live = cur >= 0;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
+                    if (!ok) break;
+                    if (p == 0 && sub == 0) ms.valid[gc & 1][key] = live;
+                    const uint32_t row = krow + (uint32_t)(2 * p) * K_ATOM;
+                    const int byte0 = (128 * p + 64 * sub) / G;
+                    const int b0 = G == 8 ? 0 : byte0 & 3;
+                    store32<G>(row, x7, 0, rec.code[p][0], rec.scale[p], b0, live);
+                    store32<G>(row, x7, 4, rec.code[p][1], rec.scale[p], b0 + 32 / G, live);
+                    filled(p);
+                    if (next >= 0) rec.load_pair(nsrc, p, sub);
+                }
+                if (!ok) break;
+                store32<G>(rrow, x7, 4 * sub, rec.rope, &rec.rope_scale,
+                           G == 8 ? 0 : (512 / G + (32 * sub) / G) & 3, live);
+                filled(4);
+                if (next >= 0) rec.load_rope(nsrc, sub);
+                cur = next;
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ITEM + (it & 1)));
+        }
+        cp_wait<0>();
+    } else {
+        fewer_registers<56>();
+        if (warp == MMA_WARP) {
+            // ---------------------------------------------------------- products
+            if (lane == 0) {
+                int it = 0, nq = 0, n16 = 0;
+                for (int w = first; w < total && ok; w += step, ++it) {
+                    ok = mbar_wait(bar(B_INFO + (it & 1)), (it >> 1) & 1, wait_ns);
+                    if (!ok) break;
+                    const Item x = ms.item[it & 1];
+                    if (x.c1 > x.c0) {
+                        // every product that reads the query tile is done: its
+                        // softmax was waited for
+                        const int hg0 = (w % nhg) * HG, id = w / nhg;
+                        const int b = id / a.nodes, t = id - b * a.nodes;
+                        const int y = (t * a.batch + b) * H + hg0;
+                        mbar_expect_tx(bar(B_Q), NATOM * Q_ATOM);
+                        for (int at = 0; at < NATOM; ++at)
+                            tma_load_2d(sQ + at * Q_ATOM, &tm_q, 64 * at, y, bar(B_Q));
+                        ++nq;
+                    }
+                    for (int c = x.c0; c < x.c1; ++c, ++gc) {
+                        const bool raw = c < x.nraw;
+                        const uint32_t idQK = idesc_f16(128, HG, raw, 0, 0);
+                        const uint32_t idPV = idesc_f16(128, 64, raw, 1, 1);
+                        if (raw && c == x.c0) ok = mbar_wait(bar(B_Q), (nq - 1) & 1, wait_ns);
+                        if (!raw && c == max(x.c0, x.nraw)) {
+                            ok = mbar_wait(bar(B_Q16), n16 & 1, wait_ns);
+                            ++n16;
+                        }
+                        for (int p = 0; p < 5 && ok; ++p) {
+                            ok = mbar_wait(bar(B_FULL + p), gc & 1, wait_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const int k1 = p < 4 ? 8 * p + 8 : 36;
+                            for (int kk = 8 * p; kk < k1; ++kk) {
+                                const uint32_t at = kk >> 2, koff = (kk & 3) * 32;
+                                mma_f16(tmem + S_COL, sdesc(sK + at * K_ATOM + koff, 16, 1024),
+                                        sdesc(sQ + at * Q_ATOM + koff, 16, 1024), idQK, kk > 0);
+                            }
+                        }
+                        if (!ok) break;
+                        mma_commit(bar(B_S));
+                        ok = mbar_wait(bar(B_P), gc & 1, wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        for (int mt = 0; mt < 4; ++mt) {
+                            for (int kk = 0; kk < CK / 16; ++kk)
+                                mma_f16(tmem + O_COL + 64 * mt,
+                                        sdesc(sK + (2 * mt) * K_ATOM + kk * 2048u, K_ATOM, 1024),
+                                        sdesc(sP + kk * 2048u, K_ATOM, 1024), idPV,
+                                        (c > x.c0 || kk > 0) ? 1u : 0u);
+                            mma_commit(bar(B_FREE + mt));
+                        }
+                    }
+                    if (!ok) break;
+                    mbar_arrive(bar(B_ITEM + (it & 1)));
+                }
+                // nothing of this CTA is in flight past here
+                mma_commit(bar(B_END));
+                mbar_wait(bar(B_END), 0, kCleanupWaitNs);
+                if (!ok && nq > 0) mbar_wait(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
+            }
+            __syncwarp();
+        } else if (warp == PATH_WARP) {
+            // -------------------------------------------------------------- path
+            int it = 0;
+            for (int w = first; w < total && ok; w += step, ++it) {
+                if (it >= 2) ok = warp_wait(B_ITEM + (it & 1), ((it >> 1) - 1) & 1);
+                if (!ok) break;
+                const int id = w / nhg;
+                const int b = id / a.nodes, t = id - b * a.nodes;
+                const int n = a.n_entries[b];
+                int wl = a.window_lens ? a.window_lens[b] : a.window_len;
+                for (int i = lane; i <= t; i += 32) {
+                    const int p = a.parents[(size_t)i * a.batch + b];
+                    ms.parents[i] = (short)(p < -2 || p >= i ? -3 : p);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const bool len_ok = n >= 0 && n <= a.capacity;
+                    if (!len_ok || wl < 0 || wl > a.window_len) set_status(a.status, KVC_DEV_BAD_LENGTH);
+                    if (wl < 0 || wl > a.window_len) wl = 0;
+                    int depth = 0, at = t;
+                    for (;;) {
+                        ms.up[it & 1][depth++] = (unsigned char)at;
+                        at = ms.parents[at];
+                        if (at >= 0) continue;
+                        if (at == -3) set_status(a.status, KVC_DEV_BAD_INDEX);
+                        if (at != -1) depth = 0;
+                        break;
+                    }
+                    Item x;
+                    x.depth = depth;
+                    x.wl = wl;
+                    x.n = len_ok ? n : -1;
+                    x.raw = depth ? min(a.window_stride, wl + depth) : 0;
+                    x.skip = wl + depth - x.raw;
+                    x.nraw = (x.raw + CK - 1) / CK;
+                    const int chunks = depth ? x.nraw + (K + CK - 1) / CK : 0;
+                    x.c0 = chunks * split / nsplit;
+                    x.c1 = chunks * (split + 1) / nsplit;
+                    ms.item[it & 1] = x;
+                    mbar_arrive(bar(B_INFO + (it & 1)));
+                }
+                __syncwarp();
+            }
+        }
+        __syncwarp();
+        more_registers<96>();
+    }
+    if (!ok && lane == 0) {
+        ms.failed = 1;
+        set_status(a.status, KVC_DEV_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // only the exchange is left: let the next kernel be scheduled
+
+    if (nsplit > 1) {
+        // ---- the CTAs of the cluster hold parts of one node: CTA r owns heads
+        // [r hpc, (r + 1) hpc) of the group.  Each stores its unnormalised O
+        // columns (a lane per channel) and (m, l) into the owners' freed K
+        // tiles, rows [split][head] of 2 KB; every owner joins them in split
+        // order.
+        const int hpc = (HG + nsplit - 1) / nsplit;
+        const int h_lo = split * hpc, nh = max(0, min(HG, h_lo + hpc) - h_lo);
+        if (tid < HG) {
+            const int r = tid / hpc, hh = tid - r * hpc;
+            const int nh_r = min(hpc, HG - r * hpc);
+            uint32_t rk, rm;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rk) : "r"(sK), "r"(r));
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                         : "=r"(rm)
+                         : "r"(smem_u32(ms.ml)), "r"(r));
+            ms.row_at[tid] = rk + (uint32_t)(split * nh_r + hh) * DV * 4;
+            ms.ml_at[tid] = rm + (uint32_t)(split * nh_r + hh) * 8;
+        }
+        const bool have = !ms.failed;
+        cluster_sync();  // every CTA of the cluster is past its last product
+        if (warp < SOFT_WARPS) {
+            const int q = warp & 3, hb = (warp >> 2) * NH;
+            const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16);
+            const bool any = have && mine;
+            if (q == 0 && lane < NH)
+                asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(ms.ml_at[hb + lane]),
+                             "f"(any ? mref : -INFINITY), "f"(any ? lv : 0.f)
+                             : "memory");
+            if (any) {
+#pragma unroll 1
+                for (int mt = 0; mt < 4; ++mt) {
+                    uint32_t o[NH];
+                    tmem_ld<NH>(ta + O_COL + 64 * mt + hb, o);
+                    tmem_wait_ld();
+                    const uint32_t d4 = (mt * 128 + q * 32 + lane) * 4;
+#pragma unroll
+                    for (int i = 0; i < NH; ++i)
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(ms.row_at[hb + i] + d4),
+                                     "r"(o[i])
+                                     : "memory");
+                }
+            }
+            tc_fence_before();
+        }
+        cluster_sync();  // every row and (m, l) has arrived
+        const int hg0 = (first % nhg) * HG, id = first / nhg;
+        const int b = id / a.nodes, t = id - b * a.nodes;
+        const size_t row = ((size_t)t * a.batch + b) * H + hg0 + h_lo;
+        if (tid < nh) {
+            float2 ml[8];
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < nsplit) {
+                    ml[r] = reinterpret_cast<const float2*>(ms.ml)[r * nh + tid];
+                    M = fmaxf(M, ml[r].x);
+                }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < nsplit) {
+                    // a split without a weight pushed no row, or one of zeros
+                    const float wt = ml[r].y == 0.f ? 0.f : ex2(ml[r].x - M);
+                    ms.wts[tid * nsplit + r] = wt;
+                    if (ml[r].y != 0.f) L += wt * ml[r].y;
+                }
+            ms.inv[tid] = L == 0.f ? 0.f : 1.f / L;
+            if (a.lse) a.lse[row + tid] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+        }
+        __syncthreads();
+        const float* rows = reinterpret_cast<const float*>(smem + OFF_K);
+        for (int i = tid; i < nh * (DV / 4); i += NT) {
+            const int hh = i / (DV / 4), q4 = i - hh * (DV / 4);
+            float wt[8];
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < nsplit) {
+                    wt[r] = ms.wts[hh * nsplit + r];
+                    v[r] = reinterpret_cast<const float4*>(rows + (r * nh + hh) * DV)[q4];
+                }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < nsplit && wt[r] != 0.f) {
+                    acc.x = fmaf(wt[r], v[r].x, acc.x);
+                    acc.y = fmaf(wt[r], v[r].y, acc.y);
+                    acc.z = fmaf(wt[r], v[r].z, acc.z);
+                    acc.w = fmaf(wt[r], v[r].w, acc.w);
+                }
+            const float inv = ms.inv[hh];
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (row + hh) * DV + 4 * q4) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem),
+                     "r"(TMEM_COLS));
+}
+
+template <int G, int HG>
+cudaError_t configure(int dev) {
+    static bool done[64] = {};
+    if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(
+        tree_t128_kernel<G, HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <int G, int HG>
+cudaError_t launch(const kvc_config& c, const Shape& sh, const TreeArgs& a, int nsplit, unsigned grid,
+                   cudaStream_t s) {
+    CUtensorMap tq = {};
+    if (!encode_rows576(&tq, a.q, (unsigned long long)a.nodes * a.batch * c.n_heads, HG))
+        return cudaErrorUnknown;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaError_t e = configure<G, HG>(dev);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = nsplit;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const float sm_log2 = c.sm_scale * 1.4426950408889634f;
+    trace_before("tree_t128", s);
+    e = cudaLaunchKernelEx(&cfg, tree_t128_kernel<G, HG>, tq, a, sh.rb, c.n_heads, c.topk, sm_log2,
+                           nsplit, device_wait_limit_ns());
+    trace_after(s);
+    return e;
+}
+
+template <int G>
+cudaError_t launch_g(const kvc_config& c, const Shape& sh, const TreeArgs& a, int hg, int nsplit,
+                     unsigned grid, cudaStream_t s) {
+    if (hg == 64) return launch<G, 64>(c, sh, a, nsplit, grid, s);
+    if (hg == 32) return launch<G, 32>(c, sh, a, nsplit, grid, s);
+    return launch<G, 16>(c, sh, a, nsplit, grid, s);
+}
+
+// Clusters of `size` of these CTAs (one a multiprocessor) that can be resident
+// at once on the current device; the kernel's variants have the same shape.
+int max_clusters(int size) {
+    static int cache[64][9] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return 0;
+    if (cache[dev][size]) return cache[dev][size] > 0 ? cache[dev][size] : 0;
+    configure<32, 64>(dev);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(size);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, tree_t128_kernel<32, 64>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    cache[dev][size] = n > 0 ? n : -1;
+    return n;
+}
+
+}  // namespace tree
+
+bool tree_t128_supported(const kvc_config& c, const Shape& sh) {
+    const bool g_ok = sh.G == 8 || sh.G == 16 || sh.G == 32 || sh.G == 64 || sh.G == 128;
+    return c.act_dtype == KVC_BF16 && c.scale_fmt == KVC_SCALE_UE4M3 && c.n_heads % 16 == 0 &&
+           sh.D == tree::D && sh.Dv == tree::DV && g_ok;
+}
+
+cudaError_t launch_tree_t128(const kvc_config& c, const Shape& sh, const TreeArgs& a,
+                             cudaStream_t s) {
+    const int H = c.n_heads;
+    const int chunks = (std::min(c.window, a.window_len + a.nodes) + tree::CK - 1) / tree::CK +
+                       (c.topk + tree::CK - 1) / tree::CK;
+    // Split of a node: the fewest chunk times until all nodes are done, a
+    // chunk of 32 or 16 heads counting 0.8 or 0.7 of one of 64, a node's
+    // start and end 1.5 chunks, an exchange 0.6.
+    int hg = 16, nsplit = 1;
+    double best = 1e30;
+    for (int g = 64; g >= 16; g /= 2) {
+        if (H % g) continue;
+        const long long items = (long long)a.nodes * a.batch * (H / g);
+        for (int ns = 1; ns <= std::min(8, std::max(1, chunks)); ++ns) {
+            const long long fit = tree::max_clusters(ns);
+            if (fit < 1) continue;
+            const double rounds = (double)((items + fit - 1) / fit);
+            const double cost = rounds * ((chunks + ns - 1) / ns * (g == 64 ? 1.0 : g == 32 ? 0.8 : 0.7) +
+                                          (ns > 1 ? 2.1 : rounds > 1 ? 0.7 : 1.5));
+            if (cost < best) best = cost, hg = g, nsplit = ns;
+        }
+    }
+    const long long items = (long long)a.nodes * a.batch * (H / hg);
+    const unsigned grid =
+        nsplit > 1 ? (unsigned)(items * nsplit)
+                   : (unsigned)std::min<long long>(items, std::max(1, tree::max_clusters(1)));
+    switch (sh.G) {
+        case 8: return tree::launch_g<8>(c, sh, a, hg, nsplit, grid, s);
+        case 16: return tree::launch_g<16>(c, sh, a, hg, nsplit, grid, s);
+        case 32: return tree::launch_g<32>(c, sh, a, hg, nsplit, grid, s);
+        case 64: return tree::launch_g<64>(c, sh, a, hg, nsplit, grid, s);
+        default: return tree::launch_g<128>(c, sh, a, hg, nsplit, grid, s);
+    }
+}
+
+}  // namespace kvc

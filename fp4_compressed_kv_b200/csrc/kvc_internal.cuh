@@ -240,6 +240,10 @@ struct TreeArgs {
     int nodes, batch, capacity, topk_shared, window_len, window_stride;
 };
 cudaError_t launch_tree(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s);
+// ... on the tensor cores (attn_tree_t128.cu), for the shapes it takes.
+bool tree_t128_supported(const kvc_config& c, const Shape& sh);
+cudaError_t launch_tree_t128(const kvc_config& c, const Shape& sh, const TreeArgs& a,
+                             cudaStream_t s);
 
 // Verification of drafted trees: rows of p and q (null: drafts taken as
 // certain) are p_ld / q_ld elements apart, node t of sequence b row t * batch + b.

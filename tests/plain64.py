@@ -84,7 +84,7 @@ def tree_attention(q, records, n_entries, capacity, topk, window, lens, draft, p
                    scale_f32):
     """cfg: (latent, rope, group, sm_scale).  Returns out, lse and the bounds'
     ingredients: sum p |v| over entries and over raw keys, the largest
-    sum |q k| of a logit, and the number of keys."""
+    sum |q k| of a logit, the number of keys, and sum |v| over entries."""
     latent, rope, group, sm = cfg
     T, B, H, D = q.shape
     W = window.shape[1]
@@ -92,6 +92,7 @@ def tree_attention(q, records, n_entries, capacity, topk, window, lens, draft, p
     lse = np.full((T, B, H), -np.inf)
     rec_abs, raw_abs = np.zeros_like(out), np.zeros_like(out)
     dots, count = np.zeros((T, B, H)), np.zeros((T, B), int)
+    rec_sum = np.zeros((T, B, 1, latent))
     for b in range(B):
         for t in range(T):
             path = path_of(parents[:, b], t)
@@ -118,7 +119,8 @@ def tree_attention(q, records, n_entries, capacity, topk, window, lens, draft, p
             out[t, b] = p @ keys[:, :latent]
             rec_abs[t, b] = p[:, :len(idx)] @ np.abs(ent[:, :latent])
             raw_abs[t, b] = p[:, len(idx):] @ np.abs(raw[:, :latent])
-    return out, lse, rec_abs, raw_abs, dots, count
+            rec_sum[t, b, 0] = np.abs(ent[:, :latent]).sum(0)
+    return out, lse, rec_abs, raw_abs, dots, count, rec_sum
 
 
 def clean(row):

@@ -8,8 +8,14 @@ Tolerances, per output channel, from the roundings alone:
           exponential's argument and result;
  weights  2 (d + 2^-22 |x|) relative, and their sums N 2^-24;
  tensor cores: weights rounded to f16 over entries (2^-11) and to bf16 over
-          raw keys (2^-8; half a step of each), f16 subnormals 2^-25 a key
-          against weights of at least 2^-8 in sum;
+          raw keys (2^-8; half a step of each).  An f16 weight below 2^-14 is
+          a multiple of 2^-24, so it is off by up to 2^-25 however small it
+          is: entry k adds up to 2^-25 |v_k|, whatever its weight.  The
+          largest weight is at least 2^7 (a reference lies 7 below the largest
+          logit of the chunk that set it, and later chunks only add), so the
+          sum of weights that divides the output is too: 2^-32 sum |v_k|
+          (sum over the entries, not weighted: where the heaviest entry holds
+          a zero, the output is made of such weights alone);
  output   half a step of its type: bf16 2^-8, fp32 2^-24.
 The log-sum-exp carries the logits' error, N 2^-24 and 2^-22 of its own."""
 import numpy as np
@@ -97,7 +103,7 @@ class Case:
 
     def check(self, want=None):
         c = self.c
-        out, lse, rec_abs, raw_abs, dots, count = want or self.expect()
+        out, lse, rec_abs, raw_abs, dots, count, rec_sum = want or self.expect()
         d = c["latent"] + c["rope"]
         logit = 2.0 ** -24 * (d / 8 + 16) * dots + 2.0 ** -22 * dots
         got, got_lse = self.out.t.double().cpu().numpy(), self.lse.t.double().cpu().numpy()
@@ -106,7 +112,7 @@ class Case:
         tol = every * (2 * logit[..., None] + n * 2.0 ** -23)
         if c["act"] == "bf16":
             tol = tol + 2.0 ** -11 * rec_abs + 2.0 ** -8 * raw_abs + 2.0 ** -8 * np.abs(out) \
-                + n * 2.0 ** -17 * every
+                + 2.0 ** -32 * rec_sum
         else:
             tol = tol + 2.0 ** -24 * np.abs(out)
         over = np.abs(got - out) - tol

@@ -15,16 +15,17 @@
 //    record chunks run in f16, where every dequantised entry is exact.  Both
 //    kinds add into the same fp32 accumulators.
 //  * One K tile of 147 KB is all that fits beside the queries, so overlap is
-//    made inside it: the latent channels are four pairs of 64-channel atoms,
-//    PV product mt is the only one that reads pair mt, and its commit frees
-//    the pair for the next chunk's values while the products mt + 1 ... run;
-//    QK of the next chunk starts on pair 0 as soon as that is filled.  Roles:
+//    made inside it: its latent channels are two halves of four 64-channel
+//    atoms, and the PV products of channels 0-255 are the only ones that read
+//    the first.  Their commit frees it for the next chunk's values while the
+//    other products run, and the next chunk's QK starts on it as soon as it is
+//    filled.  Roles:
 //      warps 0-7   softmax (thread = key, half of the heads each) and output
-//      warps 8-15  loads: the next chunk's records are in registers (two
-//                  threads a key, 32 + 32 bytes a pair and half the RoPE
-//                  codes) while this one's are converted and stored
-//      warp 16     one thread issues the products and the queries' TMA
-//      warp 17     walks the next node's path through the parents
+//      warps 8-15  loads: the next chunk's records are in registers while
+//                  this one's are converted and stored
+//      warp 16     issues the products and the queries' TMA
+//      warp 17     walks the next node's path through the parents and asks
+//                  for its selected records and queries into L2
 //    so the tensor pipe waits only for the softmax of the chunk it works on.
 //  * With many nodes a CTA takes node after node (the next node's queries,
 //    path and records arrive while this one's last products run); with few,
@@ -78,15 +79,16 @@ struct Item {  // what the roles know of one node
 
 struct Misc {
     float qs[2][64];               // softmax multiplier of the f16 queries, by item parity
-    float wmax[2][2][4][32];       // chunk maxima: [chunk parity][head half][quadrant][head]
-    float2 sm[SOFT_WARPS][32];     // each softmax warp's (multiplier, -reference)
+    float wmax[2][2][4][32];       // chunk maxima: [parity][head half][quadrant][head]
+    alignas(16) int over[2][2][4];             // a weight passes 2^kMost: [chunk parity][head half][quadrant]
+    float4 sm[SOFT_WARPS][16];     // each softmax warp's multipliers and -references, two heads
     float fac[SOFT_WARPS][32];     // each softmax warp's rescale factors
     float lsum[2][4][32];          // sums of weights: [head half][quadrant][head]
     unsigned char valid[2][CK];    // keys of the chunk that count, by chunk parity
     short parents[kMaxTreeNodes];  // path warp's
     unsigned char up[2][kMaxTreeNodes];  // ancestors k steps up, by item parity
     Item item[2];
-    uint64_t bars[24];
+    uint64_t bars[26];
     uint32_t tmem;
     int failed;
     float ml[72 * 2];              // exchange: (m, l) of [split][head]
@@ -98,8 +100,8 @@ constexpr uint32_t SMEM_BYTES = OFF_MISC + sizeof(Misc) + 1024;  // + alignment 
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 enum {
-    B_FULL = 0,   // [5] pair p (4: RoPE) of the chunk is in place (8 warps)
-    B_FREE = 5,   // [4] PV product mt is done (commit); the last covers all
+    B_FULL = 0,   // [3] half of the latent channels, RoPE of the chunk is in place (8 warps)
+    B_FREE = 3,   // [2] PV products of a half are done (commit); the second covers all
     B_S = 9,      // QK done (commit)
     B_P = 10,     // P^T is in place (8 warps)
     B_Q = 11,     // query rows landed (TMA)
@@ -108,8 +110,10 @@ enum {
     B_INFO = 15,  // [2] item of that parity published
     B_ITEM = 17,  // [2] item of that parity finished by everyone (17 warps)
     B_SUM = 19,   // [2] sums of weights of a head half (4 warps)
-    B_END = 21,
-    N_BARS = 22
+    B_OVER = 21,  // [2] checks of a head half (4 warps)
+    B_REDO = 23,  // [2] P^T of a head half is in place after all (4 warps)
+    B_END = 25,
+    N_BARS = 26
 };
 
 // A warpgroup's registers a thread.
@@ -123,6 +127,26 @@ __device__ __forceinline__ void more_registers() {
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+// mbar_wait for warps that wait long and often: each try may suspend the warp
+// for up to 20 us, so that waiting takes no issue slots from the warps at work.
+__device__ __forceinline__ bool mbar_sleep(uint32_t addr, uint32_t parity, uint64_t limit_ns) {
+    if (limit_ns == 0) return mbar_wait(addr, parity, 0);
+    uint64_t t0 = 0;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > limit_ns) return false;
+    }
 }
 __device__ __forceinline__ float warp_max(float x) {
     float y;
@@ -149,6 +173,39 @@ __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[N]) {
                          : "memory");
         asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
     }
+}
+// One lane of a converged warp.  The product warp runs as a whole and elects a
+// lane around each block of products: with warp-uniform operands a product is
+// issued in 20 clocks, where one thread's own branch takes 47 to 68 and the
+// products themselves 48.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t da, uint64_t db, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.eq.b32 p, 0, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(da), "l"(db), "r"(idesc));
+}
+// (a, b) <- (a, b) * (k.x, k.y) + (k.z, k.w)
+__device__ __forceinline__ void fma2(uint32_t& a, uint32_t& b, const float4& k) {
+    asm("{\n\t.reg .b64 x, m, c;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 m, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\t"
+        "fma.rn.f32x2 x, x, m, c;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "+r"(a), "+r"(b)
+        : "f"(k.x), "f"(k.y), "f"(k.z), "f"(k.w));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+    asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p));
 }
 // 16 bytes to shared memory, asynchronously; zeros without a source row.
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
@@ -180,26 +237,36 @@ __device__ __forceinline__ float lane_sums(float (&v)[N], int lane) {
 
 // The query tile, landed by TMA as bf16, turned into f16 in place with a power
 // of two a head that puts the row's maximum in [2^14, 2^15); the head's softmax
-// multiplier qs[h] takes it back.  Thread t: head t / 4, channels [144 (t % 4),
-// + 144) as 18 pieces of 16 bytes, read twice (maximum, then conversion) rather
-// than held: the records of the next chunk are in registers meanwhile.
-__device__ __forceinline__ void queries_to_f16(uint32_t* status, float sm_log2, uint32_t sQ,
-                                               uint32_t q_atom, float* qs, int t) {
+// multiplier qs[h] takes it back.  Thread t: head t / 4, of each 64-channel
+// atom the 16-byte pieces 2 (t % 4) and the next (eight lanes, two heads, cover
+// the eight slots of a row).  The maxima are found before the last raw product
+// is done with the tile, so that only the conversion itself waits for it; six
+// pieces are in flight at a time.
+struct QueryPart {
+    unsigned char* at[2];
+    float mul;
+};
+template <uint32_t q_atom>
+__device__ __forceinline__ void query_scale(uint32_t* status, float sm_log2, unsigned char* tile,
+                                            float* qs, int t, QueryPart& x) {
     const int h = t >> 2, qq = t & 3;
-    auto piece = [&](int i) { return sQ + ((18 * qq + i) >> 3) * q_atom + swz(h, (18 * qq + i) & 7); };
-    auto load = [&](int i, uint32_t(&w)[4]) {
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(piece(i)));
-    };
+    unsigned char* row = tile + (h >> 3) * 1024 + (h & 7) * 128;
+    x.at[0] = row + (((2 * qq) ^ (h & 7)) << 4);
+    x.at[1] = row + (((2 * qq + 1) ^ (h & 7)) << 4);
     uint32_t amax = 0;  // max |x| as fp32 bits (integer order = float order)
-#pragma unroll 6
-    for (int i = 0; i < 18; ++i) {
-        uint32_t w[4];
-        load(i, w);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+    for (int i0 = 0; i0 < 18; i0 += 6) {
+        uint4 v[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(x.at[i & 1] + ((i0 + i) >> 1) * q_atom);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                amax = max(amax, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+        }
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -209,60 +276,91 @@ __device__ __forceinline__ void queries_to_f16(uint32_t* status, float sm_log2, 
     } else if (amax != 0) {
         k = min(max((int)(amax >> 23) - 127 - 14, -60), 113);  // floor(log2 amax) - 14
     }
-    const float mul = __uint_as_float((uint32_t)(127 - k) << 23);
+    x.mul = __uint_as_float((uint32_t)(127 - k) << 23);
     if (qq == 0) qs[h] = sm_log2 * __uint_as_float((uint32_t)(127 + k) << 23);
-#pragma unroll 6
-    for (int i = 0; i < 18; ++i) {
-        uint32_t w[4];
-        load(i, w);
+}
+template <uint32_t q_atom>
+__device__ __forceinline__ void queries_to_f16(const QueryPart& x) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = pack_f16(__uint_as_float(w[j] << 16) * mul,
-                            __uint_as_float(w[j] & 0xFFFF0000u) * mul);
-        sts128(piece(i), w[0], w[1], w[2], w[3]);
+    for (int i0 = 0; i0 < 18; i0 += 6) {
+        uint4 v[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            v[i] = *reinterpret_cast<const uint4*>(x.at[i & 1] + ((i0 + i) >> 1) * q_atom);
+#pragma unroll
+        for (int i = 0; i < 6; ++i) {
+            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = pack_f16(__uint_as_float(w[j] << 16) * x.mul,
+                                __uint_as_float(w[j] & 0xFFFF0000u) * x.mul);
+            *reinterpret_cast<uint4*>(x.at[i & 1] + ((i0 + i) >> 1) * q_atom) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
 }
 
-// A thread's part of a chunk: one key, and of each pair the 64 channels of one
-// atom (32 code bytes), of the RoPE atom 32 channels (16 code bytes).  Scale
-// words: those holding the scales of these channels.
+// A load warp's part of a chunk: 16 keys.  Eight lanes read 128 code bytes of a
+// record (lane i of them 32-channel item i of a half, four keys at a time, four
+// times), so that a load touches 4 lines and not 32: the loads, the stores and
+// every barrier share one queue.  RoPE: two lanes a key.  Each item comes with
+// the word of the record that holds its scales; its bytes are taken out at the
+// store (taken out here, they would be waited for here).
 template <int G>
 struct Rec {
-    static constexpr int SW = G == 8 ? 2 : 1;
-    uint4 code[4][2];
-    uint32_t scale[4][SW];
+    uint4 code[2][4];
+    uint32_t scale[2][4];
     uint4 rope;
     uint32_t rope_scale;
-    __device__ __forceinline__ void load_pair(const uint8_t* rec, int p, int sub) {
-        code[p][0] = ldg_nc(rec + 64 * p + 32 * sub);
-        code[p][1] = ldg_nc(rec + 64 * p + 32 * sub + 16);
-        const uint32_t* sc = reinterpret_cast<const uint32_t*>(rec + 288);
-        const int first = (128 * p + 64 * sub) / G;  // scale byte of the first channel
-#pragma unroll
-        for (int i = 0; i < SW; ++i) scale[p][i] = __ldg(sc + (first >> 2) + i);
+    // channel: the item's first, counted from the start of the groups
+    static __device__ __forceinline__ uint32_t scales(const uint8_t* rec, int channel) {
+        return __ldg(reinterpret_cast<const uint32_t*>(rec + 288) + (channel / G >> 2));
     }
-    __device__ __forceinline__ void load_rope(const uint8_t* rec, int sub) {
-        rope = ldg_nc(rec + 256 + 16 * sub);
-        const int first = 512 / G + (32 * sub) / G;
-        rope_scale = __ldg(reinterpret_cast<const uint32_t*>(rec + 288) + (first >> 2));
+    static __device__ __forceinline__ int shift(int channel) { return 8 * (channel / G & 3); }
+    // Keys 4 u + (lane >> 3) of the warp's 16; idx: lane l holds key l's record.
+    // A masked key (-1) reads `none` instead, and its scales are taken as 0 at
+    // the store: loads without a branch are not waited for.
+    __device__ __forceinline__ void load_half(const uint8_t* recs, int rb, int idx,
+                                              const uint8_t* none, int half, int lane) {
+        const int item = 8 * half + (lane & 7);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int k = __shfl_sync(0xffffffffu, idx, 4 * u + (lane >> 3));
+            const uint8_t* rec = k >= 0 ? recs + (size_t)k * rb : none;
+            code[half][u] = ldg_nc(rec + 16 * item);
+            scale[half][u] = scales(rec, 32 * item);
+        }
+    }
+    __device__ __forceinline__ void load_rope(const uint8_t* recs, int rb, int idx,
+                                              const uint8_t* none, int lane) {
+        const int k = __shfl_sync(0xffffffffu, idx, lane >> 1);
+        const uint8_t* rec = k >= 0 ? recs + (size_t)k * rb : none;
+        rope = ldg_nc(rec + 256 + 16 * (lane & 1));
+        rope_scale = scales(rec, 512 + 32 * (lane & 1));
     }
 };
 
-// 32 channels (four words of codes) into 16-byte pieces c16 .. c16 + 3 of a
-// row; byte0 is the scale byte's place of the first channel in words.
+// Item `code` (32 channels, 4 words) of a row into its 16-byte pieces; step k
+// stores word k ^ j at slot z ^ k (z holds the row's swizzle, the item's half
+// of the atom and j), so that the eight lanes of a row, whose items lie in four
+// atoms, j = 0 .. 3, hit eight slots.
 template <int G>
-__device__ __forceinline__ void store32(uint32_t row, int x7, int c16, const uint4& code,
-                                        const uint32_t* words, int byte0, bool live) {
-    const uint32_t c[4] = {code.x, code.y, code.z, code.w};
+__device__ __forceinline__ void store_item(unsigned char* row, int z, int j, const uint4& code,
+                                           uint32_t scale) {
+    uint32_t c[4] = {code.x, code.y, code.z, code.w};
+    if (j) {
+        const uint32_t a0 = j & 1 ? c[1] : c[0], a1 = j & 1 ? c[0] : c[1];
+        const uint32_t a2 = j & 1 ? c[3] : c[2], a3 = j & 1 ? c[2] : c[3];
+        c[0] = j & 2 ? a2 : a0, c[1] = j & 2 ? a3 : a1;
+        c[2] = j & 2 ? a0 : a2, c[3] = j & 2 ? a1 : a3;
+    }
+    uint32_t s2 = ue4m3_f16x2(scale & 0xFFu);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (live) {
-            const int sb = byte0 + (8 * k) / G;
-            const uint32_t word = G == 8 ? words[sb >> 2] : words[0];
-            e2m1x8_scaled(c[k], ue4m3_f16x2((word >> (8 * (sb & 3))) & 0xFFu), w);
-        }
-        sts128(row + (((uint32_t)(c16 + k) ^ x7) << 4), w[0], w[1], w[2], w[3]);
+        if (G < 32) s2 = ue4m3_f16x2((scale >> (G == 8 ? 8 * (k ^ j) : 8 * ((k ^ j) >> 1))) & 0xFFu);
+        uint32_t w[4];
+        e2m1x8_scaled(c[k], s2, w);
+        *reinterpret_cast<uint4*>(row + ((z ^ k) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -281,7 +379,8 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     const uint32_t bars = smem_u32(ms.bars);
     auto bar = [&](int i) { return bars + 8u * i; };
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // (known to be warp-uniform)
     const int split = blockIdx.x % nsplit;
     const int first = blockIdx.x / nsplit, step = gridDim.x / nsplit;
     const int nhg = H / HG, total = a.nodes * a.batch * nhg;
@@ -294,10 +393,11 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     }
     if (tid == 0) {
         for (int i = 0; i < N_BARS; ++i) {
-            const int count = i < B_FREE || i == B_P || i == B_Q16 ? 8
-                              : i == B_MAX || i == B_MAX + 1 || i == B_SUM || i == B_SUM + 1 ? 4
-                              : i == B_ITEM || i == B_ITEM + 1     ? 17
-                                                                   : 1;
+            const int count = i < B_FREE || i == B_P || i == B_Q16     ? 8
+                              : i == B_MAX || i == B_MAX + 1           ? 4
+                              : i == B_ITEM || i == B_ITEM + 1         ? 17
+                              : i >= B_SUM && i < B_END                ? 4
+                                                                       : 1;
             mbar_init(bar(i), count);
         }
         ms.failed = 0;
@@ -316,7 +416,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                                        // lane (of the warp's half)
     // A whole warp's wait: its lanes leave with one answer.
     auto warp_wait = [&](int i, int parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar(i), parity, wait_ns)) != 0;
+        return __all_sync(0xffffffffu, mbar_sleep(bar(i), parity, wait_ns)) != 0;
     };
     // The item's facts, once the path warp has published them.
     auto get_item = [&](int it, Item& x) {
@@ -334,7 +434,8 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
         const int q = warp & 3, half = warp >> 2, hb = half * NH;
         const int s = q * 32 + lane;  // key of a chunk, tensor-memory lane
         const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16);
-        int it = 0, nsum = 0;
+        unsigned char* prow = smem + OFF_P + (s >> 3) * 1024 + (s & 7) * 128;  // P^T of the key
+        int it = 0, nsum = 0, nmax = 0, nover = 0;
         for (int w = first; w < total && ok; w += step, ++it) {
             Item x;
             if (!get_item(it, x)) break;
@@ -351,75 +452,124 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 if (!ok) break;
                 tc_fence_after();
                 const bool valid = ms.valid[gc & 1][s];
-                uint32_t r[NH];
-                tmem_ld<NH>(ta + S_COL + hb, r);
-                tmem_wait_ld();
-                // the chunk's maximum of every head: over the warp's keys, then
-                // over the four quadrants
-                float mx = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < NH; ++i) {
-                    if (!valid) r[i] = 0xFF800000u;  // -inf
-                    const float m = warp_max(__uint_as_float(r[i]));
-                    if (lane == i) mx = m;
-                }
-                float(&wm)[4][32] = ms.wmax[gc & 1][half];
-                wm[q][lane] = mx;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_MAX + half));
-                ok = warp_wait(B_MAX + half, gc & 1);
-                if (!ok) break;
-                const float my = fmaxf(fmaxf(wm[0][lane], wm[1][lane]), fmaxf(wm[2][lane], wm[3][lane]));
                 const float mul = raw || lane >= NH ? sm_log2 : ms.qs[it & 1][hb + lane];
-                const float mc = my * mul;
-                const float mo = mref;
-                const float mn = (mo == -INFINITY || mc > mo + kMost) ? mc - kTop : mo;
-                const float f = mo == -INFINITY ? 1.f : ex2(mo - mn);
-                mref = mn;
-                ms.sm[warp][lane] = make_float2(mul, mn == -INFINITY ? 0.f : -mn);
-                ms.fac[warp][lane] = f;
-                const bool moved = __any_sync(0xffffffffu, lane < NH && c > x.c0 && f != 1.f);
-                if (moved)
+                uint32_t r[NH];
+                auto logits = [&]() {
+                    tmem_ld<NH>(ta + S_COL + hb, r);
+                    tmem_wait_ld();
+                    if (!__all_sync(0xffffffffu, valid))
 #pragma unroll
-                    for (int i = 0; i < NH; ++i) l[i] *= ms.fac[warp][i];
-                // weights 2^(x - reference) of the key, a 16-byte piece of 8 heads at a time
+                        for (int i = 0; i < NH; ++i) r[i] = valid ? r[i] : 0xFF800000u;  // -inf
+                };
+                auto factors = [&]() {
+                    float* k = reinterpret_cast<float*>(&ms.sm[warp][lane >> 1]) + (lane & 1);
+                    k[0] = mul;
+                    k[2] = mref == -INFINITY ? 0.f : -mref;
+                    __syncwarp();
+                };
+                // weights 2^(x - reference) of the key in place of its logits,
+                // and P^T; returns the largest exponent
+                auto weights = [&]() {
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int c8 = 0; c8 < NH / 8; ++c8) {
-                    uint32_t v[4];
+                    for (int c8 = 0; c8 < NH / 8; ++c8) {
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int h = 8 * c8 + 2 * u;
-                        const float4 k = *reinterpret_cast<const float4*>(&ms.sm[warp][h]);
-                        const float p0 = ex2(fmaf(__uint_as_float(r[h]), k.x, k.y));
-                        const float p1 = ex2(fmaf(__uint_as_float(r[h + 1]), k.z, k.w));
-                        l[h] += p0;
-                        l[h + 1] += p1;
-                        v[u] = raw ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+                        for (int u = 0; u < 4; ++u) {
+                            uint32_t &p0 = r[8 * c8 + 2 * u], &p1 = r[8 * c8 + 2 * u + 1];
+                            fma2(p0, p1, ms.sm[warp][4 * c8 + u]);
+                            mx = max3(mx, __uint_as_float(p0), __uint_as_float(p1));
+                            p0 = __float_as_uint(ex2(__uint_as_float(p0)));
+                            p1 = __float_as_uint(ex2(__uint_as_float(p1)));
+                        }
+                        uint32_t v[4];
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) {
+                            const float p0 = __uint_as_float(r[8 * c8 + 2 * u]);
+                            const float p1 = __uint_as_float(r[8 * c8 + 2 * u + 1]);
+                            v[u] = raw ? pack_bf16(p0, p1) : pack_f16(p0, p1);
+                        }
+                        *reinterpret_cast<uint4*>(prow + ((((hb >> 3) + c8) ^ (s & 7)) << 4)) =
+                            make_uint4(v[0], v[1], v[2], v[3]);
                     }
-                    sts128(sP + swz(s, (hb >> 3) + c8), v[0], v[1], v[2], v[3]);
-                }
-                fence_async_smem();
-                if (moved) {
-                    // rare: a reference moved by more than the slack: what the
-                    // accumulators hold of the earlier chunks is rescaled
-                    ok = warp_wait(B_FREE + 3, (gc - 1) & 1);
+                    return mx;
+                };
+                auto in_place = [&](int i) {
+                    fence_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(i));
+                };
+                // The references of the earlier chunks nearly always serve: the
+                // weights are made with them at once.  Where one of this head
+                // half passes 2^kMost, the products are told to wait until the
+                // half has done it over with the chunk's own maxima, as the
+                // first chunk does.
+                bool fresh = c == x.c0;
+                logits();
+                if (!fresh) {
+                    if (c == x.nraw) factors();  // other multipliers from here on
+                    // (a head without a key so far has no reference)
+                    const bool over = __any_sync(
+                        0xffffffffu, weights() > kMost || (lane < NH && mref == -INFINITY));
+                    int(&ov)[4] = ms.over[gc & 1][half];
+                    if (lane == 0) {
+                        ov[q] = over;
+                        mbar_arrive(bar(B_OVER + half));
+                    }
+                    in_place(B_P);
+                    ok = warp_wait(B_OVER + half, nover++ & 1);
                     if (!ok) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int t = 0; t < 4; ++t) {
-                        const uint32_t at = ta + O_COL + 64 * t + hb;
-                        uint32_t o[NH];
-                        tmem_ld<NH>(at, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < NH; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * ms.fac[warp][i]);
-                        tmem_st<NH>(at, o);
-                    }
+                    fresh = ov[0] | ov[1] | ov[2] | ov[3];
+                    if (fresh) logits();
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_P));
+                if (fresh) {
+                    // the chunk's maximum of every head: over the warp's keys,
+                    // then over the four quadrants
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NH; ++i) {
+                        const float m = warp_max(__uint_as_float(r[i]));
+                        if (lane == i) mx = m;
+                    }
+                    float(&wm)[4][32] = ms.wmax[nmax & 1][half];
+                    wm[q][lane] = mx;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_MAX + half));
+                    ok = warp_wait(B_MAX + half, nmax++ & 1);
+                    if (!ok) break;
+                    const float mc = mul * fmaxf(fmaxf(wm[0][lane], wm[1][lane]),
+                                                 fmaxf(wm[2][lane], wm[3][lane]));
+                    const float mo = mref;
+                    if (mo == -INFINITY || mc > mo + kMost) mref = mc - kTop;
+                    const float f = mo == -INFINITY ? 1.f : ex2(mo - mref);
+                    ms.fac[warp][lane] = f;
+                    factors();
+                    if (__any_sync(0xffffffffu, lane < NH && c > x.c0 && f != 1.f)) {
+                        // a reference moved: what the sums and accumulators
+                        // hold of the earlier chunks is rescaled
+                        ok = warp_wait(B_FREE + 1, (gc - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int t = 0; t < 4; ++t) {
+                            const uint32_t at = ta + O_COL + 64 * t + hb;
+                            uint32_t o[NH];
+                            tmem_ld<NH>(at, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < NH; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * ms.fac[warp][i]);
+                            tmem_st<NH>(at, o);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NH; ++i) l[i] *= ms.fac[warp][i];
+                        logits();
+                    }
+                    weights();
+                    in_place(c == x.c0 ? B_P : B_REDO + half);
+                }
+#pragma unroll
+                for (int i = 0; i < NH; ++i) l[i] += __uint_as_float(r[i]);
             }
             if (!ok) break;
             if (x.c1 > x.c0) {
@@ -427,7 +577,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 ls[q][lane] = lane_sums<NH>(l, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SUM + half));
-                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 3, (gc - 1) & 1);
+                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 1, (gc - 1) & 1);
                 if (!ok) break;
                 lv = (ls[0][lane] + ls[1][lane]) + (ls[2][lane] + ls[3][lane]);
                 tc_fence_after();
@@ -473,10 +623,12 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     } else if (warp < SOFT_WARPS + LOAD_WARPS) {
         // ------------------------------------------------------------- loads
         const int lw = warp - SOFT_WARPS;
-        const int key = lw * 16 + (lane & 7) + ((lane >> 4) << 3), sub = (lane >> 3) & 1;
-        const uint32_t x7 = key & 7;
-        const uint32_t krow = sK + (uint32_t)sub * K_ATOM + (uint32_t)(key >> 3) * 1024u + x7 * 128u;
-        const uint32_t rrow = sK + 8 * K_ATOM + (uint32_t)(key >> 3) * 1024u + x7 * 128u;
+        const int row0 = lw * 16;  // the warp's keys
+        const int kq = lane >> 3, j8 = (lane & 7) >> 1;
+        const int z0 = ((4 * (lane & 1)) | j8) ^ kq;
+        unsigned char* krow = smem + OFF_K + (row0 >> 3) * 1024 + kq * 128 + j8 * K_ATOM;
+        const int rkey = row0 + (lane >> 1);  // RoPE: two lanes a key
+        unsigned char* rrow = smem + OFF_K + 8 * K_ATOM + (rkey >> 3) * 1024 + (rkey & 7) * 128;
         auto filled = [&](int p) {
             fence_async_smem();
             __syncwarp();
@@ -491,74 +643,92 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             const int node = t * a.batch + b;
             const int32_t* sel = a.topk_idx + (a.topk_shared ? (size_t)b : (size_t)node) * K;
             const uint8_t* recs = a.records + (size_t)b * a.capacity * rb;
-            // record of this thread's key in chunk c, or -1
+            // (a query row is longer than a record)
+            const uint8_t* none = static_cast<const uint8_t*>(a.q);
+            // record of key row0 + lane (lanes below 16) in chunk c, or -1
             auto pick = [&](int c) {
-                const int j = (c - x.nraw) * CK + key;
+                const int j = (c - x.nraw) * CK + row0 + (lane & 15);
                 if (j >= K || x.n < 0) return -1;
                 const int idx = __ldg(sel + j);
                 if (idx >= 0 && idx < x.n) return idx;
-                if (idx != -1 && sub == 0 && hg0 == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
+                if (idx != -1 && lane < 16 && hg0 == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
                 return -1;
             };
             Rec<G> rec;
             int cur = -1;
             const int cr = max(x.c0, x.nraw);  // first record chunk
-            if (cr < x.c1) {
-                cur = pick(cr);
-                if (cur >= 0) {
-                    const uint8_t* src = recs + (size_t)cur * rb;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) rec.load_pair(src, p, sub);
-                    rec.load_rope(src, sub);
-                }
-            }
+            auto first_records = [&]() {
+                rec.load_half(recs, rb, cur, none, 0, lane);
+                rec.load_half(recs, rb, cur, none, 1, lane);
+                rec.load_rope(recs, rb, cur, none, lane);
+            };
+            if (cr < x.c1) cur = pick(cr);
+            // (behind the first node's raw copies: the index is on its way)
+            const bool early = gc > 0 || x.c0 >= x.nraw;
+            if (early && cr < x.c1) first_records();
             // ---- raw chunks
             int c = x.c0;
             for (; c < min(x.nraw, x.c1); ++c, ++gc) {
-                const int j = c * CK + key, r = x.skip + j;
-                const bool live = j < x.raw;
-                const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.draft);
-                if (live)
-                    src = r < x.wl ? static_cast<const __nv_bfloat16*>(a.window) +
+                // lane l < 16 finds row l of the warp's; eight lanes then copy 128
+                // bytes of a row, four rows at a time
+                const int j = c * CK + row0 + (lane & 15), r = x.skip + j;
+                const __nv_bfloat16* mine_row = nullptr;
+                if (j < x.raw)
+                    mine_row = r < x.wl
+                                   ? static_cast<const __nv_bfloat16*>(a.window) +
                                          ((size_t)b * a.window_stride + r) * D
-                                   : src + ((size_t)ms.up[it & 1][x.depth - 1 - (r - x.wl)] * a.batch +
-                                            b) * D;
-#pragma unroll 1
-                for (int p = 0; p < 4 && ok; ++p) {
-                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
-                    if (!ok) break;
+                                   : static_cast<const __nv_bfloat16*>(a.draft) +
+                                         ((size_t)ms.up[it & 1][x.depth - 1 - (r - x.wl)] * a.batch +
+                                          b) * D;
+                const uint32_t piece = lane & 7;
+                const __nv_bfloat16* src[4];
+                uint32_t dst[4];
+                uint32_t live = 0;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        cp16(krow + (uint32_t)(2 * p) * K_ATOM + (((uint32_t)k ^ x7) << 4),
-                             src + (2 * p + sub) * 64 + 8 * k, live);
+                for (int k = 0; k < 4; ++k) {
+                    const unsigned long long from = __shfl_sync(
+                        0xffffffffu, reinterpret_cast<unsigned long long>(mine_row), 4 * k + kq);
+                    live |= (from != 0) << k;
+                    src[k] = (from ? reinterpret_cast<const __nv_bfloat16*>(from)
+                                   : static_cast<const __nv_bfloat16*>(a.draft)) + 8 * piece;
+                    dst[k] = sK + swz(row0 + 4 * k + kq, piece);
+                }
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (gc > 0) ok = warp_wait(B_FREE + h, (gc - 1) & 1);
+                    if (!ok) break;
+                    if (h == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = mine_row != nullptr;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        cp16(dst[k & 3] + (4 * h + (k >> 2)) * K_ATOM,
+                             src[k & 3] + (4 * h + (k >> 2)) * 64, live >> (k & 3) & 1);
                     cp_commit();
                 }
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    cp16(rrow + (((uint32_t)(4 * sub + k) ^ x7) << 4), src + 512 + 32 * sub + 8 * k,
-                         live);
+                    cp16(dst[k] + 8 * K_ATOM, src[k] + 512, live >> k & 1);
                 cp_commit();
-                if (sub == 0) ms.valid[gc & 1][key] = live;
-                cp_wait<4>();
-                filled(0);
-                cp_wait<3>();
-                filled(1);
+                if (!early && c == x.c0 && cr < x.c1) first_records();
                 cp_wait<2>();
-                filled(2);
+                filled(0);
                 cp_wait<1>();
-                filled(3);
+                filled(1);
                 cp_wait<0>();
-                filled(4);
+                filled(2);
             }
             if (!ok) break;
             // ---- the queries to f16, once the raw chunks' products have read them
             if (cr < x.c1) {
                 ok = warp_wait(B_Q, nq & 1);
-                if (ok && c > x.c0) ok = warp_wait(B_S, (gc - 1) & 1);
                 if (!ok) break;
                 const int ct = tid - SOFT_WARPS * 32;
-                if (ct < 4 * HG) queries_to_f16(a.status, sm_log2, sQ, Q_ATOM, ms.qs[it & 1], ct);
+                QueryPart part;
+                if (ct < 4 * HG)
+                    query_scale<Q_ATOM>(a.status, sm_log2, smem + OFF_Q, ms.qs[it & 1], ct, part);
+                if (c > x.c0) ok = warp_wait(B_S, (gc - 1) & 1);
+                if (!ok) break;
+                if (ct < 4 * HG) queries_to_f16<Q_ATOM>(part);
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_Q16));
@@ -567,26 +737,32 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             // ---- record chunks
             for (; c < x.c1; ++c, ++gc) {
                 const int next = c + 1 < x.c1 ? pick(c + 1) : -1;
-                const uint8_t* nsrc = recs + (size_t)(next < 0 ? 0 : next) * rb;
-                const bool live = cur >= 0;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
+                for (int h = 0; h < 2; ++h) {
+                    if (gc > 0) ok = warp_wait(B_FREE + h, (gc - 1) & 1);
                     if (!ok) break;
-                    if (p == 0 && sub == 0) ms.valid[gc & 1][key] = live;
-                    const uint32_t row = krow + (uint32_t)(2 * p) * K_ATOM;
-                    const int byte0 = (128 * p + 64 * sub) / G;
-                    const int b0 = G == 8 ? 0 : byte0 & 3;
-                    store32<G>(row, x7, 0, rec.code[p][0], rec.scale[p], b0, live);
-                    store32<G>(row, x7, 4, rec.code[p][1], rec.scale[p], b0 + 32 / G, live);
-                    filled(p);
-                    if (next >= 0) rec.load_pair(nsrc, p, sub);
+                    if (h == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = cur >= 0;
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const bool live = __shfl_sync(0xffffffffu, cur, 4 * u + kq) >= 0;
+                        const uint32_t sc = rec.scale[h][u] >> Rec<G>::shift(32 * (8 * h + (lane & 7)));
+                        store_item<G>(krow + 4 * h * K_ATOM + (u >> 1) * 1024 + (u & 1) * 512,
+                                      z0 ^ (4 * (u & 1)), j8, rec.code[h][u], live ? sc : 0u);
+                    }
+                    filled(h);
                 }
                 if (!ok) break;
-                store32<G>(rrow, x7, 4 * sub, rec.rope, &rec.rope_scale,
-                           G == 8 ? 0 : (512 / G + (32 * sub) / G) & 3, live);
-                filled(4);
-                if (next >= 0) rec.load_rope(nsrc, sub);
+                const bool live = __shfl_sync(0xffffffffu, cur, lane >> 1) >= 0;
+                store_item<G>(rrow, (4 * (lane & 1)) ^ (rkey & 7), 0, rec.rope,
+                              live ? rec.rope_scale >> Rec<G>::shift(512 + 32 * (lane & 1)) : 0u);
+                filled(2);
+                // all loads behind the chunk's stores: issuing them takes a
+                // thousand clocks, which lie under QK and the softmax here
+                if (c + 1 < x.c1) {
+                    rec.load_half(recs, rb, next, none, 0, lane);
+                    rec.load_half(recs, rb, next, none, 1, lane);
+                    rec.load_rope(recs, rb, next, none, lane);
+                }
                 cur = next;
             }
             if (!ok) break;
@@ -598,61 +774,93 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
         fewer_registers<56>();
         if (warp == MMA_WARP) {
             // ---------------------------------------------------------- products
-            if (lane == 0) {
-                int it = 0, nq = 0, n16 = 0;
-                for (int w = first; w < total && ok; w += step, ++it) {
-                    ok = mbar_wait(bar(B_INFO + (it & 1)), (it >> 1) & 1, wait_ns);
-                    if (!ok) break;
-                    const Item x = ms.item[it & 1];
-                    if (x.c1 > x.c0) {
-                        // every product that reads the query tile is done: its
-                        // softmax was waited for
-                        const int hg0 = (w % nhg) * HG, id = w / nhg;
-                        const int b = id / a.nodes, t = id - b * a.nodes;
-                        const int y = (t * a.batch + b) * H + hg0;
+            int it = 0, nq = 0, n16 = 0, nredo0 = 0, nredo1 = 0;
+            // operand descriptors; offsets are in units of 16 bytes
+            const uint64_t kd = sdesc(sK, 16, 1024), qd = sdesc(sQ, 16, 1024);
+            const uint64_t vd = sdesc(sK, K_ATOM, 1024), pd = sdesc(sP, K_ATOM, 1024);
+            for (int w = first; w < total && ok; w += step, ++it) {
+                Item x;
+                if (!get_item(it, x)) break;
+                if (x.c1 > x.c0) {
+                    // every product that reads the query tile is done: its
+                    // softmax was waited for
+                    const int hg0 = (w % nhg) * HG, id = w / nhg;
+                    const int b = id / a.nodes, t = id - b * a.nodes;
+                    const int y = (t * a.batch + b) * H + hg0;
+                    if (lane == 0) {
                         mbar_expect_tx(bar(B_Q), NATOM * Q_ATOM);
                         for (int at = 0; at < NATOM; ++at)
                             tma_load_2d(sQ + at * Q_ATOM, &tm_q, 64 * at, y, bar(B_Q));
-                        ++nq;
                     }
-                    for (int c = x.c0; c < x.c1; ++c, ++gc) {
-                        const bool raw = c < x.nraw;
-                        const uint32_t idQK = idesc_f16(128, HG, raw, 0, 0);
-                        const uint32_t idPV = idesc_f16(128, 64, raw, 1, 1);
-                        if (raw && c == x.c0) ok = mbar_wait(bar(B_Q), (nq - 1) & 1, wait_ns);
-                        if (!raw && c == max(x.c0, x.nraw)) {
-                            ok = mbar_wait(bar(B_Q16), n16 & 1, wait_ns);
-                            ++n16;
-                        }
-                        for (int p = 0; p < 5 && ok; ++p) {
-                            ok = mbar_wait(bar(B_FULL + p), gc & 1, wait_ns);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const int k1 = p < 4 ? 8 * p + 8 : 36;
-                            for (int kk = 8 * p; kk < k1; ++kk) {
-                                const uint32_t at = kk >> 2, koff = (kk & 3) * 32;
-                                mma_f16(tmem + S_COL, sdesc(sK + at * K_ATOM + koff, 16, 1024),
-                                        sdesc(sQ + at * Q_ATOM + koff, 16, 1024), idQK, kk > 0);
-                            }
-                        }
-                        if (!ok) break;
-                        mma_commit(bar(B_S));
-                        ok = mbar_wait(bar(B_P), gc & 1, wait_ns);
+                    __syncwarp();
+                    ++nq;
+                }
+                for (int c = x.c0; c < x.c1; ++c, ++gc) {
+                    const bool raw = c < x.nraw;
+                    const uint32_t idQK = idesc_f16(128, HG, raw, 0, 0);
+                    const uint32_t idPV = idesc_f16(128, 64, raw, 1, 1);
+                    if (raw && c == x.c0) ok = warp_wait(B_Q, (nq - 1) & 1);
+                    if (!raw && c == max(x.c0, x.nraw)) ok = warp_wait(B_Q16, n16++ & 1);
+#pragma unroll 1
+                    for (int h = 0; h < 2 && ok; ++h) {
+                        ok = warp_wait(B_FULL + h, gc & 1);
                         if (!ok) break;
                         tc_fence_after();
-                        for (int mt = 0; mt < 4; ++mt) {
-                            for (int kk = 0; kk < CK / 16; ++kk)
-                                mma_f16(tmem + O_COL + 64 * mt,
-                                        sdesc(sK + (2 * mt) * K_ATOM + kk * 2048u, K_ATOM, 1024),
-                                        sdesc(sP + kk * 2048u, K_ATOM, 1024), idPV,
-                                        (c > x.c0 || kk > 0) ? 1u : 0u);
-                            mma_commit(bar(B_FREE + mt));
+                        if (elect()) {
+                            const uint64_t ka = kd + h * (4 * K_ATOM >> 4);
+                            const uint64_t qa = qd + h * (4 * Q_ATOM >> 4);
+                            mma_f16(tmem + S_COL, ka, qa, idQK, h);
+#pragma unroll
+                            for (int kk = 1; kk < 16; ++kk)
+                                mma(tmem + S_COL, ka + (kk >> 2) * (K_ATOM >> 4) + (kk & 3) * 2,
+                                    qa + (kk >> 2) * (Q_ATOM >> 4) + (kk & 3) * 2, idQK);
                         }
+                        __syncwarp();
+                    }
+                    ok = ok && warp_wait(B_FULL + 2, gc & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect()) {  // the RoPE atom
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma(tmem + S_COL, kd + (8 * K_ATOM >> 4) + kk * 2,
+                                qd + (8 * Q_ATOM >> 4) + kk * 2, idQK);
+                        mma_commit(bar(B_S));
+                    }
+                    __syncwarp();
+                    ok = warp_wait(B_P, gc & 1);
+                    if (ok && c > x.c0) {  // a head half that does its weights over
+                        const int4 o0 = *reinterpret_cast<const int4*>(ms.over[gc & 1][0]);
+                        const int4 o1 = *reinterpret_cast<const int4*>(ms.over[gc & 1][1]);
+                        if (o0.x | o0.y | o0.z | o0.w) ok = warp_wait(B_REDO, nredo0++ & 1);
+                        if (ok && (o1.x | o1.y | o1.z | o1.w))
+                            ok = warp_wait(B_REDO + 1, nredo1++ & 1);
                     }
                     if (!ok) break;
-                    mbar_arrive(bar(B_ITEM + (it & 1)));
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        if (elect()) {
+#pragma unroll
+                            for (int mt = 0; mt < 2; ++mt) {
+                                const uint32_t o = tmem + O_COL + 128 * h + 64 * mt;
+                                const uint64_t va = vd + (2 * h + mt) * (2 * K_ATOM >> 4);
+                                mma_f16(o, va, pd, idPV, c > x.c0);
+#pragma unroll
+                                for (int kk = 1; kk < CK / 16; ++kk)
+                                    mma(o, va + kk * 128, pd + kk * 128, idPV);
+                            }
+                            mma_commit(bar(B_FREE + h));
+                        }
+                        __syncwarp();
+                    }
                 }
-                // nothing of this CTA is in flight past here
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(B_ITEM + (it & 1)));
+            }
+            // nothing of this CTA is in flight past here (the elected lane is
+            // the same throughout, so its commit covers every product)
+            if (elect()) {
                 mma_commit(bar(B_END));
                 mbar_wait(bar(B_END), 0, kCleanupWaitNs);
                 if (!ok && nq > 0) mbar_wait(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
@@ -700,10 +908,24 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     mbar_arrive(bar(B_INFO + (it & 1)));
                 }
                 __syncwarp();
+                if (it > 0) {  // (a CTA's first node is being loaded already)
+                    const int node = t * a.batch + b;
+                    const int32_t* sel = a.topk_idx + (a.topk_shared ? (size_t)b : (size_t)node) * K;
+                    const uint8_t* recs = a.records + (size_t)b * a.capacity * rb;
+                    const char* qrow = static_cast<const char*>(a.q) +
+                                       ((size_t)node * H + (w % nhg) * HG) * D * 2;
+                    for (int i = lane; i < (int)(NATOM * Q_ATOM) / 128; i += 32)
+                        prefetch_l2(qrow + 128 * i);
+                    for (int j = lane; j < K; j += 32) {
+                        const int idx = __ldg(sel + j);
+                        if (idx >= 0 && idx < min(n, a.capacity))
+                            for (int o = 0; o < rb; o += 128)
+                                prefetch_l2(recs + (size_t)idx * rb + o);
+                    }
+                }
             }
         }
         __syncwarp();
-        more_registers<96>();
     }
     if (!ok && lane == 0) {
         ms.failed = 1;
@@ -711,6 +933,9 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     }
     tc_fence_before();
     __syncthreads();
+    // (only now: a warp that waits for registers to be free takes issue slots
+    // from the others of its scheduler)
+    if (warp >= MMA_WARP) more_registers<96>();
     tc_fence_after();
     pdl_trigger();  // only the exchange is left: let the next kernel be scheduled
 

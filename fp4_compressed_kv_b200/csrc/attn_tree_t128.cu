@@ -15,10 +15,10 @@
 //    record chunks run in f16, where every dequantised entry is exact.  Both
 //    kinds add into the same fp32 accumulators.
 //  * One K tile of 147 KB is all that fits beside the queries, so overlap is
-//    made inside it: its latent channels are two halves of four 64-channel
-//    atoms, and the PV products of channels 0-255 are the only ones that read
-//    the first.  Their commit frees it for the next chunk's values while the
-//    other products run, and the next chunk's QK starts on it as soon as it is
+//    made inside it: its latent channels are four pairs of 64-channel atoms,
+//    and the PV products of channels 128 p ... are the only ones that read pair
+//    p.  Their commit frees it for the next chunk's values while the other
+//    products run, and the next chunk's QK starts on it as soon as it is
 //    filled.  Roles:
 //      warps 0-7   softmax (thread = key, half of the heads each) and output
 //      warps 8-15  loads: the next chunk's records are in registers while
@@ -100,8 +100,8 @@ constexpr uint32_t SMEM_BYTES = OFF_MISC + sizeof(Misc) + 1024;  // + alignment 
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 enum {
-    B_FULL = 0,   // [3] half of the latent channels, RoPE of the chunk is in place (8 warps)
-    B_FREE = 3,   // [2] PV products of a half are done (commit); the second covers all
+    B_FULL = 0,   // [5] a pair (4: the RoPE atom) of the chunk is in place (8 warps)
+    B_FREE = 5,   // [4] PV products of a pair are done (commit); the last covers all
     B_S = 9,      // QK done (commit)
     B_P = 10,     // P^T is in place (8 warps)
     B_Q = 11,     // query rows landed (TMA)
@@ -300,16 +300,16 @@ __device__ __forceinline__ void queries_to_f16(const QueryPart& x) {
     }
 }
 
-// A load warp's part of a chunk: 16 keys.  Eight lanes read 128 code bytes of a
-// record (lane i of them 32-channel item i of a half, four keys at a time, four
-// times), so that a load touches 4 lines and not 32: the loads, the stores and
-// every barrier share one queue.  RoPE: two lanes a key.  Each item comes with
-// the word of the record that holds its scales; its bytes are taken out at the
-// store (taken out here, they would be waited for here).
+// A load warp's part of a chunk: 16 keys.  Of each pair four lanes read the 64
+// code bytes of a record (eight keys at a time, twice), so that a load touches
+// 8 lines and not 32: the loads, the stores and every barrier share one queue.
+// RoPE: two lanes a key.  Each item of 32 channels comes with the word of the
+// record that holds its scales; its bytes are taken out at the store (taken out
+// here, they would be waited for here).
 template <int G>
 struct Rec {
-    uint4 code[2][4];
-    uint32_t scale[2][4];
+    uint4 code[4][2];
+    uint32_t scale[4][2];
     uint4 rope;
     uint32_t rope_scale;
     // channel: the item's first, counted from the start of the groups
@@ -317,19 +317,21 @@ struct Rec {
         return __ldg(reinterpret_cast<const uint32_t*>(rec + 288) + (channel / G >> 2));
     }
     static __device__ __forceinline__ int shift(int channel) { return 8 * (channel / G & 3); }
-    // Keys 4 u + (lane >> 3) of the warp's 16; idx: lane l holds key l's record.
-    // A masked key (-1) reads `none` instead, and its scales are taken as 0 at
-    // the store: loads without a branch are not waited for.
-    __device__ __forceinline__ void load_half(const uint8_t* recs, int rb, int idx,
-                                              const uint8_t* none, int half, int lane) {
-        const int item = 8 * half + (lane & 7);
+    // idx: lane l holds key l's record.  A masked key (-1) reads `none` instead,
+    // and its scales are taken as 0 at the store.
+    __device__ __forceinline__ void load(const uint8_t* recs, int rb, int idx, const uint8_t* none,
+                                         int lane) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int k = __shfl_sync(0xffffffffu, idx, 4 * u + (lane >> 3));
+        for (int u = 0; u < 2; ++u) {
+            const int k = __shfl_sync(0xffffffffu, idx, 8 * u + (lane >> 2));
             const uint8_t* rec = k >= 0 ? recs + (size_t)k * rb : none;
-            code[half][u] = ldg_nc(rec + 16 * item);
-            scale[half][u] = scales(rec, 32 * item);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                code[p][u] = ldg_nc(rec + 16 * (4 * p + (lane & 3)));
+                scale[p][u] = scales(rec, 32 * (4 * p + (lane & 3)));
+            }
         }
+        load_rope(recs, rb, idx, none, lane);
     }
     __device__ __forceinline__ void load_rope(const uint8_t* recs, int rb, int idx,
                                               const uint8_t* none, int lane) {
@@ -341,23 +343,18 @@ struct Rec {
 };
 
 // Item `code` (32 channels, 4 words) of a row into its 16-byte pieces; step k
-// stores word k ^ j at slot z ^ k (z holds the row's swizzle, the item's half
-// of the atom and j), so that the eight lanes of a row, whose items lie in four
-// atoms, j = 0 .. 3, hit eight slots.
+// stores word k ^ 2 j at slot z ^ k (z holds the row's swizzle, the item's half
+// of the atom and 2 j), so that eight lanes, two rows of items in two atoms
+// (j = 0, 1), hit eight slots.
 template <int G>
 __device__ __forceinline__ void store_item(unsigned char* row, int z, int j, const uint4& code,
                                            uint32_t scale) {
-    uint32_t c[4] = {code.x, code.y, code.z, code.w};
-    if (j) {
-        const uint32_t a0 = j & 1 ? c[1] : c[0], a1 = j & 1 ? c[0] : c[1];
-        const uint32_t a2 = j & 1 ? c[3] : c[2], a3 = j & 1 ? c[2] : c[3];
-        c[0] = j & 2 ? a2 : a0, c[1] = j & 2 ? a3 : a1;
-        c[2] = j & 2 ? a0 : a2, c[3] = j & 2 ? a1 : a3;
-    }
+    const uint32_t c[4] = {j ? code.z : code.x, j ? code.w : code.y, j ? code.x : code.z,
+                           j ? code.y : code.w};
     uint32_t s2 = ue4m3_f16x2(scale & 0xFFu);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if (G < 32) s2 = ue4m3_f16x2((scale >> (G == 8 ? 8 * (k ^ j) : 8 * ((k ^ j) >> 1))) & 0xFFu);
+        if (G < 32) s2 = ue4m3_f16x2((scale >> (G == 8 ? 8 * (k ^ 2 * j) : 8 * ((k >> 1) ^ j))) & 0xFFu);
         uint32_t w[4];
         e2m1x8_scaled(c[k], s2, w);
         *reinterpret_cast<uint4*>(row + ((z ^ k) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -547,7 +544,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     if (__any_sync(0xffffffffu, lane < NH && c > x.c0 && f != 1.f)) {
                         // a reference moved: what the sums and accumulators
                         // hold of the earlier chunks is rescaled
-                        ok = warp_wait(B_FREE + 1, (gc - 1) & 1);
+                        ok = warp_wait(B_FREE + 3, (gc - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -577,7 +574,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 ls[q][lane] = lane_sums<NH>(l, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SUM + half));
-                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 1, (gc - 1) & 1);
+                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 3, (gc - 1) & 1);
                 if (!ok) break;
                 lv = (ls[0][lane] + ls[1][lane]) + (ls[2][lane] + ls[3][lane]);
                 tc_fence_after();
@@ -624,9 +621,10 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
         // ------------------------------------------------------------- loads
         const int lw = warp - SOFT_WARPS;
         const int row0 = lw * 16;  // the warp's keys
-        const int kq = lane >> 3, j8 = (lane & 7) >> 1;
-        const int z0 = ((4 * (lane & 1)) | j8) ^ kq;
-        unsigned char* krow = smem + OFF_K + (row0 >> 3) * 1024 + kq * 128 + j8 * K_ATOM;
+        const int kq = lane >> 3;  // raw rows: eight lanes a row
+        const int k8 = lane >> 2, j = (lane >> 1) & 1;  // records: four lanes a key
+        const int z = (4 * (lane & 1)) ^ (2 * j) ^ k8;
+        unsigned char* krow = smem + OFF_K + (row0 >> 3) * 1024 + k8 * 128 + j * K_ATOM;
         const int rkey = row0 + (lane >> 1);  // RoPE: two lanes a key
         unsigned char* rrow = smem + OFF_K + 8 * K_ATOM + (rkey >> 3) * 1024 + (rkey & 7) * 128;
         auto filled = [&](int p) {
@@ -657,15 +655,10 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             Rec<G> rec;
             int cur = -1;
             const int cr = max(x.c0, x.nraw);  // first record chunk
-            auto first_records = [&]() {
-                rec.load_half(recs, rb, cur, none, 0, lane);
-                rec.load_half(recs, rb, cur, none, 1, lane);
-                rec.load_rope(recs, rb, cur, none, lane);
-            };
             if (cr < x.c1) cur = pick(cr);
             // (behind the first node's raw copies: the index is on its way)
             const bool early = gc > 0 || x.c0 >= x.nraw;
-            if (early && cr < x.c1) first_records();
+            if (early && cr < x.c1) rec.load(recs, rb, cur, none, lane);
             // ---- raw chunks
             int c = x.c0;
             for (; c < min(x.nraw, x.c1); ++c, ++gc) {
@@ -694,14 +687,14 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     dst[k] = sK + swz(row0 + 4 * k + kq, piece);
                 }
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (gc > 0) ok = warp_wait(B_FREE + h, (gc - 1) & 1);
+                for (int p = 0; p < 4; ++p) {
+                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
                     if (!ok) break;
-                    if (h == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = mine_row != nullptr;
+                    if (p == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = mine_row != nullptr;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        cp16(dst[k & 3] + (4 * h + (k >> 2)) * K_ATOM,
-                             src[k & 3] + (4 * h + (k >> 2)) * 64, live >> (k & 3) & 1);
+                    for (int k = 0; k < 8; ++k)
+                        cp16(dst[k & 3] + (2 * p + (k >> 2)) * K_ATOM,
+                             src[k & 3] + (2 * p + (k >> 2)) * 64, live >> (k & 3) & 1);
                     cp_commit();
                 }
                 if (!ok) break;
@@ -709,13 +702,17 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 for (int k = 0; k < 4; ++k)
                     cp16(dst[k] + 8 * K_ATOM, src[k] + 512, live >> k & 1);
                 cp_commit();
-                if (!early && c == x.c0 && cr < x.c1) first_records();
-                cp_wait<2>();
+                if (!early && c == x.c0 && cr < x.c1) rec.load(recs, rb, cur, none, lane);
+                cp_wait<4>();
                 filled(0);
-                cp_wait<1>();
+                cp_wait<3>();
                 filled(1);
-                cp_wait<0>();
+                cp_wait<2>();
                 filled(2);
+                cp_wait<1>();
+                filled(3);
+                cp_wait<0>();
+                filled(4);
             }
             if (!ok) break;
             // ---- the queries to f16, once the raw chunks' products have read them
@@ -737,32 +734,32 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             // ---- record chunks
             for (; c < x.c1; ++c, ++gc) {
                 const int next = c + 1 < x.c1 ? pick(c + 1) : -1;
+                bool keep[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (gc > 0) ok = warp_wait(B_FREE + h, (gc - 1) & 1);
+                for (int u = 0; u < 2; ++u)
+                    keep[u] = __shfl_sync(0xffffffffu, cur, 8 * u + k8) >= 0;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
                     if (!ok) break;
-                    if (h == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = cur >= 0;
+                    if (p == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = cur >= 0;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const bool live = __shfl_sync(0xffffffffu, cur, 4 * u + kq) >= 0;
-                        const uint32_t sc = rec.scale[h][u] >> Rec<G>::shift(32 * (8 * h + (lane & 7)));
-                        store_item<G>(krow + 4 * h * K_ATOM + (u >> 1) * 1024 + (u & 1) * 512,
-                                      z0 ^ (4 * (u & 1)), j8, rec.code[h][u], live ? sc : 0u);
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t sc =
+                            rec.scale[p][u] >> Rec<G>::shift(32 * (4 * p + (lane & 3)));
+                        store_item<G>(krow + 2 * p * K_ATOM + u * 1024, z, j, rec.code[p][u],
+                                      keep[u] ? sc : 0u);
                     }
-                    filled(h);
+                    filled(p);
                 }
                 if (!ok) break;
                 const bool live = __shfl_sync(0xffffffffu, cur, lane >> 1) >= 0;
                 store_item<G>(rrow, (4 * (lane & 1)) ^ (rkey & 7), 0, rec.rope,
                               live ? rec.rope_scale >> Rec<G>::shift(512 + 32 * (lane & 1)) : 0u);
-                filled(2);
+                filled(4);
                 // all loads behind the chunk's stores: issuing them takes a
                 // thousand clocks, which lie under QK and the softmax here
-                if (c + 1 < x.c1) {
-                    rec.load_half(recs, rb, next, none, 0, lane);
-                    rec.load_half(recs, rb, next, none, 1, lane);
-                    rec.load_rope(recs, rb, next, none, lane);
-                }
+                if (c + 1 < x.c1) rec.load(recs, rb, next, none, lane);
                 cur = next;
             }
             if (!ok) break;
@@ -802,22 +799,22 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     if (raw && c == x.c0) ok = warp_wait(B_Q, (nq - 1) & 1);
                     if (!raw && c == max(x.c0, x.nraw)) ok = warp_wait(B_Q16, n16++ & 1);
 #pragma unroll 1
-                    for (int h = 0; h < 2 && ok; ++h) {
-                        ok = warp_wait(B_FULL + h, gc & 1);
+                    for (int p = 0; p < 4 && ok; ++p) {
+                        ok = warp_wait(B_FULL + p, gc & 1);
                         if (!ok) break;
                         tc_fence_after();
                         if (elect()) {
-                            const uint64_t ka = kd + h * (4 * K_ATOM >> 4);
-                            const uint64_t qa = qd + h * (4 * Q_ATOM >> 4);
-                            mma_f16(tmem + S_COL, ka, qa, idQK, h);
+                            const uint64_t ka = kd + p * (2 * K_ATOM >> 4);
+                            const uint64_t qa = qd + p * (2 * Q_ATOM >> 4);
+                            mma_f16(tmem + S_COL, ka, qa, idQK, p > 0);
 #pragma unroll
-                            for (int kk = 1; kk < 16; ++kk)
+                            for (int kk = 1; kk < 8; ++kk)
                                 mma(tmem + S_COL, ka + (kk >> 2) * (K_ATOM >> 4) + (kk & 3) * 2,
                                     qa + (kk >> 2) * (Q_ATOM >> 4) + (kk & 3) * 2, idQK);
                         }
                         __syncwarp();
                     }
-                    ok = ok && warp_wait(B_FULL + 2, gc & 1);
+                    ok = ok && warp_wait(B_FULL + 4, gc & 1);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect()) {  // the RoPE atom
@@ -839,18 +836,15 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
+                    for (int p = 0; p < 4; ++p) {
                         if (elect()) {
+                            const uint32_t o = tmem + O_COL + 64 * p;
+                            const uint64_t va = vd + p * (2 * K_ATOM >> 4);
+                            mma_f16(o, va, pd, idPV, c > x.c0);
 #pragma unroll
-                            for (int mt = 0; mt < 2; ++mt) {
-                                const uint32_t o = tmem + O_COL + 128 * h + 64 * mt;
-                                const uint64_t va = vd + (2 * h + mt) * (2 * K_ATOM >> 4);
-                                mma_f16(o, va, pd, idPV, c > x.c0);
-#pragma unroll
-                                for (int kk = 1; kk < CK / 16; ++kk)
-                                    mma(o, va + kk * 128, pd + kk * 128, idPV);
-                            }
-                            mma_commit(bar(B_FREE + h));
+                            for (int kk = 1; kk < CK / 16; ++kk)
+                                mma(o, va + kk * 128, pd + kk * 128, idPV);
+                            mma_commit(bar(B_FREE + p));
                         }
                         __syncwarp();
                     }

@@ -400,6 +400,18 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
         ms.failed = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    if (nsplit > 1 && tid < HG) {  // where each head's owner takes this CTA's sums
+        const int hpc = (HG + nsplit - 1) / nsplit;
+        const int r = tid / hpc, hh = tid - r * hpc;
+        const int nh_r = min(hpc, HG - r * hpc);
+        uint32_t rk, rm;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rk) : "r"(sK), "r"(r));
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(rm)
+                     : "r"(smem_u32(ms.ml)), "r"(r));
+        ms.row_at[tid] = rk + (uint32_t)(split * nh_r + hh) * DV * 4;
+        ms.ml_at[tid] = rm + (uint32_t)(split * nh_r + hh) * 8;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -633,6 +645,12 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             if (lane == 0) mbar_arrive(bar(B_FULL + p));
         };
         int it = 0, nq = 0;
+        if (first < total) {  // the first node's selection, while its path is walked
+            const int id = first / nhg, b = id / a.nodes, t = id - b * a.nodes;
+            const int32_t* sel = a.topk_idx + (size_t)(a.topk_shared ? b : t * a.batch + b) * K;
+            for (int j = tid - SOFT_WARPS * 32; j < (K + 31) / 32; j += LOAD_WARPS * 32)
+                prefetch_l2(sel + 32 * j);
+        }
         for (int w = first; w < total && ok; w += step, ++it) {
             Item x;
             if (!get_item(it, x)) break;
@@ -852,12 +870,14 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(bar(B_ITEM + (it & 1)));
             }
-            // nothing of this CTA is in flight past here (the elected lane is
-            // the same throughout, so its commit covers every product)
-            if (elect()) {
+            // Nothing of this CTA is in flight past here: the softmax waited for
+            // the last products; after a timeout they and the queries' copies
+            // are waited for now (the elected lane is the same throughout, so
+            // its commit covers every product).
+            if (!ok && elect()) {
                 mma_commit(bar(B_END));
-                mbar_wait(bar(B_END), 0, kCleanupWaitNs);
-                if (!ok && nq > 0) mbar_wait(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
+                mbar_sleep(bar(B_END), 0, kCleanupWaitNs);
+                if (nq > 0) mbar_sleep(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
             }
             __syncwarp();
         } else if (warp == PATH_WARP) {
@@ -941,17 +961,6 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
         // order.
         const int hpc = (HG + nsplit - 1) / nsplit;
         const int h_lo = split * hpc, nh = max(0, min(HG, h_lo + hpc) - h_lo);
-        if (tid < HG) {
-            const int r = tid / hpc, hh = tid - r * hpc;
-            const int nh_r = min(hpc, HG - r * hpc);
-            uint32_t rk, rm;
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(rk) : "r"(sK), "r"(r));
-            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                         : "=r"(rm)
-                         : "r"(smem_u32(ms.ml)), "r"(r));
-            ms.row_at[tid] = rk + (uint32_t)(split * nh_r + hh) * DV * 4;
-            ms.ml_at[tid] = rm + (uint32_t)(split * nh_r + hh) * 8;
-        }
         const bool have = !ms.failed;
         cluster_sync();  // every CTA of the cluster is past its last product
         if (warp < SOFT_WARPS) {
@@ -1128,20 +1137,27 @@ cudaError_t launch_tree_t128(const kvc_config& c, const Shape& sh, const TreeArg
     const int H = c.n_heads;
     const int chunks = (std::min(c.window, a.window_len + a.nodes) + tree::CK - 1) / tree::CK +
                        (c.topk + tree::CK - 1) / tree::CK;
-    // Split of a node: the fewest chunk times until all nodes are done, a
-    // chunk of 32 or 16 heads counting 0.8 or 0.7 of one of 64, a node's
-    // start and end 1.5 chunks, an exchange 0.6.
+    // Split of a node's keys over nsplit CTAs and of its heads into groups of hg:
+    // the least of what follows, in microseconds as measured on one sequence's
+    // node to 256 nodes of 5 chunks (64 heads; in brackets measured).  A CTA
+    // that takes whole nodes: 10 + rounds x (chunks x c + 1) [1 node 33.8, 256
+    // nodes 60.4]; a cluster that splits them: 5 + rounds x (chunks / nsplit x c
+    // + e) [1 node over 5 CTAs 23.5, in groups of 16 heads 18.6], where a chunk
+    // takes c = 4.5, 3.9, 3.6 and a start, exchange and end e = 14, 12, 10 for
+    // 64, 32, 16 heads.
     int hg = 16, nsplit = 1;
     double best = 1e30;
     for (int g = 64; g >= 16; g /= 2) {
         if (H % g) continue;
         const long long items = (long long)a.nodes * a.batch * (H / g);
+        const double ct = g == 64 ? 4.5 : g == 32 ? 3.9 : 3.6;
+        const double et = g == 64 ? 14.0 : g == 32 ? 12.0 : 10.0;
         for (int ns = 1; ns <= std::min(8, std::max(1, chunks)); ++ns) {
             const long long fit = tree::max_clusters(ns);
             if (fit < 1) continue;
             const double rounds = (double)((items + fit - 1) / fit);
-            const double cost = rounds * ((chunks + ns - 1) / ns * (g == 64 ? 1.0 : g == 32 ? 0.8 : 0.7) +
-                                          (ns > 1 ? 2.1 : rounds > 1 ? 0.7 : 1.5));
+            const double cost = ns == 1 ? 10.0 + rounds * (chunks * ct + 1.0)
+                                        : 5.0 + rounds * ((chunks + ns - 1) / ns * ct + et);
             if (cost < best) best = cost, hg = g, nsplit = ns;
         }
     }

@@ -16,22 +16,31 @@
 //
 // Everything that decides (products, masses, running sums) is fp64: the
 // products of two fp32 numbers are exact and a border is moved by 10^-16 of
-// the mass, where fp32 sums of 10^5 terms would move it past whole tokens.
+// the mass, where fp32 sums of 10^5 terms would move it past whole tokens.  No
+// value is converted: an fp32 pattern moved up by 29 bits is the same number
+// times 2^-896 in fp64, subnormals and 0 included, so a pass works on residuals
+// of that scale (two shifts an entry, where a conversion takes a warp 8 clocks)
+// and scales their sum back.
 //
 // A sequence is one cluster of CTAs, each with a contiguous share of the
-// vocabulary in chunks of 1024; sums of the shares are exchanged over
-// distributed shared memory, so every CTA walks the tree alike.  What each
-// node's walk looks up (token, parent, u, p(x), q(x)) is loaded by one thread
-// a node at the start.  Bound: the rows of the last accepted node and of every
-// node with a rejection, read from HBM.
+// vocabulary in blocks of 128 entries (more where a share has more than 1024
+// of them), a block to a warp, two in flight; the sums of the shares are
+// exchanged over distributed shared memory, so every CTA walks the tree alike.
+// What each node's walk looks up (token, parent, u, p(x), q(x)) is loaded by
+// one thread a node at the start.  Bound: the rows of the last accepted node
+// and of every node with a rejection, read from HBM once and from the caches
+// in later passes; small batches by the chain of a pass, two dependent loads
+// and a cluster barrier for each rejection.
 #include "kvc_internal.cuh"
 
 namespace kvc {
 namespace {
 
 constexpr int NT = 512, NW = NT / 32;
-constexpr int CHUNK = 1024;   // vocabulary entries of one warp's share of a pass
-constexpr int MAX_CLUSTER = 8;
+constexpr int BLOCK = 128;  // vocabulary entries a warp sums at a time
+constexpr int NB = 2;       // blocks of a warp in flight
+constexpr int MAX_CLUSTER = 8, MAX_BLOCKS = 1024;
+constexpr double kScaleUp = 0x1p896;
 
 __device__ __forceinline__ float as_f32(float x) { return x; }
 __device__ __forceinline__ float as_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -57,24 +66,32 @@ __device__ __forceinline__ double warp_scan(double x, int lane) {  // inclusive
     return x;
 }
 
-// Entries e .. e + 3 of a row as floats; past the vocabulary 0.
+// Entries e .. e + 3 of a row as fp32 patterns; past the vocabulary 0.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T* row, int e, int vocab, float (&v)[4]) {
+__device__ __forceinline__ void load4(const T* row, int e, int vocab, uint32_t (&v)[4]) {
     if constexpr (VEC) {
         if (e + 4 <= vocab) {
             if constexpr (sizeof(T) == 4) {
-                const float4 f = __ldg(reinterpret_cast<const float4*>(row + e));
-                v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + e));
+                v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
             } else {
                 const uint2 w = __ldg(reinterpret_cast<const uint2*>(row + e));
-                v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xFFFF0000u);
-                v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xFFFF0000u);
+                v[0] = w.x << 16, v[1] = w.x & 0xFFFF0000u;
+                v[2] = w.y << 16, v[3] = w.y & 0xFFFF0000u;
             }
             return;
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = e + j < vocab ? as_f32(row[e + j]) : 0.f;
+    for (int j = 0; j < 4; ++j) v[j] = e + j < vocab ? __float_as_uint(as_f32(row[e + j])) : 0u;
+}
+// A pattern as it counts: negative values, NaN and infinities are 0.
+__device__ __forceinline__ uint32_t clean(uint32_t x, bool& bad) {
+    bad |= (x & 0x7F800000u) == 0x7F800000u;
+    return x < 0x7F800000u ? x : 0u;
+}
+__device__ __forceinline__ double scaled(uint32_t x) {  // value x 2^-896
+    return __hiloint2double((int)(x >> 3), (int)(x << 29));
 }
 
 struct NodeFacts {
@@ -82,55 +99,66 @@ struct NodeFacts {
     float u, p, q;  // q: 1 without draft probabilities
 };
 
-// The residual of 4 entries: max(p - S q, 0), or p without the rejected tokens.
+// The residual max(p - S q, 0) (without q: p without the rejected tokens).
+template <typename T>
 struct Residual {
+    const T* p;
+    const T* q;  // or null
     double S;
     const int* gone;  // rejected tokens (no draft probabilities)
     int n_gone;
 };
 
-// Residual values of a chunk's entries e = c0 + 4 lane + 128 i + j, summed
-// into the warp's total; r receives them when given.
-template <typename T, bool VEC>
-__device__ __forceinline__ double chunk_pass(const T* p, const T* q, int c0, int vocab,
-                                             const Residual& res, int lane, bool& bad, double* r) {
-    double sum = 0.0;
-    bool any_gone = false;
-    for (int g = 0; g < res.n_gone; ++g)
-        any_gone |= res.gone[g] >= c0 && res.gone[g] < c0 + CHUNK;
-    float pv[8][4], qv[8][4];
+// N quads of entries e[i] .. e[i] + 3 of this lane as patterns, cleaned and
+// without the rejected tokens (e[i] >= vocab: zeros).
+template <typename T, bool VEC, int N>
+__device__ __forceinline__ void load_quads(const Residual<T>& res, const int (&e)[N], int vocab,
+                                           uint32_t (&pv)[N][4], uint32_t (&qv)[N][4], bool& bad) {
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        load4<T, VEC>(p, c0 + 4 * lane + 128 * i, vocab, pv[i]);
-        if (q) load4<T, VEC>(q, c0 + 4 * lane + 128 * i, vocab, qv[i]);
-    }
+    for (int i = 0; i < N; ++i) load4<T, VEC>(res.p, e[i], vocab, pv[i]);
+    if (res.q)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i) load4<T, VEC>(res.q, e[i], vocab, qv[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int e = c0 + 4 * lane + 128 * i + j;
-            double x = (double)counts(pv[i][j], bad);
-            if (q) x = fmax(fma(-res.S, (double)counts(qv[i][j], bad), x), 0.0);
-            if (any_gone)
-                for (int g = 0; g < res.n_gone; ++g)
-                    if (res.gone[g] == e) x = 0.0;
-            if (r) r[(e - c0) + ((e - c0) >> 5)] = x;
-            sum += x;
+            if (!res.q) qv[i][j] = 0u;
+            most = max(most, max(pv[i][j], qv[i][j]));
         }
-    return warp_sum(sum);
+    if (most >= 0x7F800000u)  // rare: something that is no finite probability
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                pv[i][j] = clean(pv[i][j], bad);
+                qv[i][j] = clean(qv[i][j], bad);
+            }
+    for (int g = 0; g < res.n_gone; ++g) {
+        const int t = res.gone[g];
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (t == e[i] + j) pv[i][j] = 0u;
+    }
+}
+// Residual of one entry, times 2^-896.
+__device__ __forceinline__ double residual(uint32_t p, uint32_t q, double S) {
+    const double x = fma(-S, scaled(q), scaled(p));
+    return x > 0.0 ? x : 0.0;
 }
 
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(NT)
-verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
+__global__ void __launch_bounds__(NT, 2)
+verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
     extern __shared__ __align__(16) unsigned char smem[];
-    NodeFacts* facts = reinterpret_cast<NodeFacts*>(smem);               // [nodes]
-    int* gone = reinterpret_cast<int*>(facts + a.nodes);                 // [nodes]
-    double* csum = reinterpret_cast<double*>(
-        smem + ((a.nodes * (sizeof(NodeFacts) + 4) + 15) & ~(size_t)15));  // [chunks_per_cta]
-    double* rbuf = csum + chunks_per_cta;                                // [CHUNK + CHUNK / 32]
+    NodeFacts* facts = reinterpret_cast<NodeFacts*>(smem);  // [nodes]
+    int* gone = reinterpret_cast<int*>(facts + a.nodes);    // [nodes]
+    double* bsum = reinterpret_cast<double*>(                // [blocks_per_cta], times 2^-896
+        smem + ((a.nodes * (sizeof(NodeFacts) + 4) + 15) & ~(size_t)15));
     __shared__ double share[2][MAX_CLUSTER];  // every CTA's sum of the pass, by its parity
-    __shared__ double wsum[NW];
     const int b = blockIdx.x / cluster, rank = blockIdx.x - b * cluster;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const T* pb = static_cast<const T*>(a.p);
@@ -168,27 +196,50 @@ verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
     int cur = 0, n_path = 1, n_gone = 0, passes = 0;
     double S = 0.0, m = 1.0;
     bool summed = false;  // csum and share hold the residual of `cur` at S
-    const int chunk_lo = rank * chunks_per_cta;
-    const int n_chunks = min(chunks_per_cta, (a.vocab + CHUNK - 1) / CHUNK - chunk_lo);
+    const int width = BLOCK * nsub;  // entries of a block
+    const int first_block = rank * blocks_per_cta;
+    const int n_blocks = min(blocks_per_cta, (a.vocab + width - 1) / width - first_block);
+    auto residual_of = [&](bool use_q) {
+        const size_t row = (size_t)cur * a.batch + b;
+        return Residual<T>{pb + row * a.p_ld, use_q ? qb + row * a.q_ld : nullptr, use_q ? S : 0.0,
+                           gone, n_gone};
+    };
     // One pass over this CTA's share of the residual; returns its whole mass.
     auto pass = [&](bool use_q) -> double {
-        const size_t row = (size_t)cur * a.batch + b;
-        const Residual res = {S, gone, n_gone};
-        double mine = 0.0;
-        for (int c = warp; c < n_chunks; c += NW) {
-            const double s = chunk_pass<T, VEC>(pb + row * a.p_ld,
-                                                use_q ? qb + row * a.q_ld : nullptr,
-                                                (chunk_lo + c) * CHUNK, a.vocab, res, lane, bad,
-                                                nullptr);
-            if (lane == 0) csum[c] = s;
-            mine += s;
+        const Residual<T> res = residual_of(use_q);
+        for (int b0 = warp; b0 < n_blocks; b0 += NW * NB) {
+            double s[NB] = {};
+            for (int sub = 0; sub < nsub; ++sub) {
+                int e[NB];
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    e[i] = b0 + NW * i < n_blocks
+                               ? (first_block + b0 + NW * i) * width + sub * BLOCK + 4 * lane
+                               : a.vocab;
+                uint32_t pv[NB][4], qv[NB][4];
+                load_quads<T, VEC, NB>(res, e, a.vocab, pv, qv, bad);
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const double x = fma(-res.S, scaled(qv[i][j]), scaled(pv[i][j]));
+                        if (x > 0.0) s[i] += x;
+                    }
+            }
+            // block sums: lanes 16 k .. 16 k + 15 end with that of block k
+            const double send = lane & 16 ? s[0] : s[1], keep = lane & 16 ? s[1] : s[0];
+            s[0] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+#pragma unroll
+            for (int o = 8; o >= 1; o >>= 1) s[0] += __shfl_xor_sync(0xffffffffu, s[0], o);
+            const int k = b0 + NW * (lane >> 4);
+            if ((lane & 15) == 0 && k < n_blocks) bsum[k] = s[0];
         }
-        if (lane == 0) wsum[warp] = mine;
         __syncthreads();
         const int par = passes & 1;
         ++passes;
         if (warp == 0) {
-            double t = lane < NW ? wsum[lane] : 0.0;
+            double t = 0.0;
+            for (int k = lane; k < n_blocks; k += 32) t += bsum[k];
             t = warp_sum(t);
             if (lane < cluster) {
                 uint32_t dst;
@@ -201,7 +252,7 @@ verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
                      "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         double sum = 0.0;
         for (int r = 0; r < cluster; ++r) sum += share[par][r];
-        return sum;
+        return sum * kScaleUp;
     };
 
     if (rank == 0 && tid == 0 && !absent) a.path[(size_t)b * a.nodes] = 0;
@@ -249,9 +300,12 @@ verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
             m = pass(false);
         }
         // the CTA whose share the draw falls into (the last one with any mass
-        // where rounding leaves none), its chunk, and the entry
+        // where rounding leaves none), its block, and the entry; all of it at
+        // the scale of the sums
         const double* sh = share[(passes - 1) & 1];
-        const double target = (double)a.v[b] * m;
+        double whole = 0.0;
+        for (int r = 0; r < cluster; ++r) whole += sh[r];
+        const double target = (double)a.v[b] * whole;
         double before = 0.0;
         int owner = -1;
         for (int r = 0; r < cluster; ++r) {
@@ -266,45 +320,60 @@ verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
                 bad = true;
             }
         } else if (owner == rank && warp == 0) {
-            int chunk = -1;
-            double base = before;   // running sum in front of `chunk`
-            double run = before;
-            for (int c0 = 0; c0 < n_chunks; c0 += 32) {
-                const double mine = c0 + lane < n_chunks ? csum[c0 + lane] : 0.0;
+            // Among values in order, the first whose running sum passes the
+            // target, or the last with any mass: `found`, with `base` the sum in
+            // front of it.
+            int found = -1;
+            double base = before, run = before;
+            auto step = [&](double mine, int first) {  // one value a lane
                 const double upto = run + warp_scan(mine, lane);
                 const unsigned hit = __ballot_sync(0xffffffffu, mine > 0.0 && upto > target);
                 const unsigned pos = __ballot_sync(0xffffffffu, mine > 0.0);
                 const int at = hit ? __ffs(hit) - 1 : (pos ? 31 - __clz(pos) : -1);
                 if (at >= 0) {
-                    chunk = c0 + at;
+                    found = first + at;
                     base = __shfl_sync(0xffffffffu, upto - mine, at);
                 }
-                if (hit) break;
                 run = __shfl_sync(0xffffffffu, upto, 31);
+                return hit != 0;
+            };
+            for (int k = 0; k < n_blocks; k += 32)
+                if (step(k + lane < n_blocks ? bsum[k + lane] : 0.0, k)) break;
+            const int e0 = (first_block + found) * width;
+            const Residual<T> res = residual_of(use_q);
+            run = base;
+            found = -1;
+            double r[4], in_quad[4] = {};
+            for (int sub = 0; sub < nsub; ++sub) {
+                const int e[1] = {e0 + sub * BLOCK + 4 * lane};
+                uint32_t pv[1][4], qv[1][4];
+                load_quads<T, VEC, 1>(res, e, a.vocab, pv, qv, bad);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = residual(pv[0][j], qv[0][j], res.S);
+                const int was = found;
+                const bool done = step((r[0] + r[1]) + (r[2] + r[3]), 32 * sub);
+                if (found != was)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) in_quad[j] = r[j];
+                if (done) break;
             }
-            const size_t row = (size_t)cur * a.batch + b;
-            const Residual res = {S, gone, n_gone};
-            const int c0 = (chunk_lo + chunk) * CHUNK;
-            chunk_pass<T, VEC>(pb + row * a.p_ld, use_q ? qb + row * a.q_ld : nullptr, c0, a.vocab,
-                               res, lane, bad, rbuf);
-            __syncwarp();
-            double mine = 0.0;
-            for (int i = 0; i < 32; ++i) mine += rbuf[33 * lane + i];
-            const double upto = base + warp_scan(mine, lane);
-            const unsigned hit = __ballot_sync(0xffffffffu, mine > 0.0 && upto > target);
-            const unsigned pos = __ballot_sync(0xffffffffu, mine > 0.0);
-            const int at = hit ? __ffs(hit) - 1 : 31 - __clz(pos);
-            if (lane == at) {
-                double x = upto - mine;
-                int found = 0;
-                for (int i = 0; i < 32; ++i) {
-                    const double r = rbuf[33 * lane + i];
-                    if (!(r > 0.0)) continue;
-                    found = i;
-                    x += r;
-                    if (x > target) break;
+            if (lane == (found & 31)) {
+                double x = base;
+                int at = 0;
+#pragma unroll
+                for (int j = 3; j >= 0; --j)  // the last with any mass ...
+                    if (in_quad[j] > 0.0) {
+                        at = j;
+                        break;
+                    }
+                for (int j = 0; j < 4; ++j) {  // ... unless the target is passed
+                    x += in_quad[j];
+                    if (in_quad[j] > 0.0 && x > target) {
+                        at = j;
+                        break;
+                    }
                 }
-                a.next[b] = c0 + 32 * lane + found;
+                a.next[b] = e0 + 4 * found + at;
             }
         }
     } else if (rank == 0 && tid == 0) {
@@ -323,22 +392,17 @@ verify_kernel(VerifyArgs a, int cluster, int chunks_per_cta) {
 
 template <typename T, bool VEC>
 cudaError_t launch_v(const VerifyArgs& a, cudaStream_t s) {
-    const int chunks = (a.vocab + CHUNK - 1) / CHUNK;
+    // CTAs of a sequence: while each keeps a block for every warp and all of
+    // them run at once (two a multiprocessor)
+    const int quads = (a.vocab + BLOCK - 1) / BLOCK;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && cluster * 2 <= chunks && a.batch * cluster * 2 <= 148 * 4)
+    while (cluster < MAX_CLUSTER && quads >= 2 * cluster * NW && a.batch * cluster * 2 <= 148 * 2)
         cluster *= 2;
-    const int per = (chunks + cluster - 1) / cluster;
-    const size_t smem = ((a.nodes * (sizeof(NodeFacts) + 4) + 15) & ~(size_t)15) +
-                        ((size_t)per + CHUNK + CHUNK / 32) * 8;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    static bool attr_set[64] = {};
-    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            verify_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
-        if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
-    }
+    int nsub = 1;
+    while ((quads + nsub * cluster - 1) / (nsub * cluster) > MAX_BLOCKS) nsub *= 2;
+    const int blocks = (quads + nsub - 1) / nsub;
+    const int per = (blocks + cluster - 1) / cluster;
+    const size_t smem = ((a.nodes * (sizeof(NodeFacts) + 4) + 15) & ~(size_t)15) + (size_t)per * 8;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)a.batch * cluster);
     cfg.blockDim = dim3(NT);
@@ -354,7 +418,7 @@ cudaError_t launch_v(const VerifyArgs& a, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     trace_before("verify", s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, a, cluster, per);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_kernel<T, VEC>, a, cluster, per, nsub);
     trace_after(s);
     return e;
 }

@@ -123,27 +123,35 @@ def _stream(stream):
     return C.c_void_p(s.cuda_stream)
 
 
-def _operand(name, t, dtype, shape, contiguous=True):
+def _here(stream):
+    """Current device and the address of `stream` on it (None: the current
+    stream, without the 3 us that torch.cuda.current_stream() takes)."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _operand(name, t, dtype, shape, dev, contiguous=True):
     """Device address of an operand (None stays None), checked: type, shape,
-    contiguity, and that it lives on the current device (the library's work
-    and pointers belong to it)."""
+    contiguity, and that it lives on the current device `dev` (the library's
+    work and pointers belong to it)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype == dtype and t.shape == shape and t.get_device() == dev and \
+            (not contiguous or t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current CUDA device")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
 def _act(cfg: Config):
     return torch.bfloat16 if cfg.act_dtype == BF16 else torch.float32
 
 
-def _status(status):
-    return None if status is None else _operand("status", status, torch.int32, (1,))
+def _status(status, dev):
+    return None if status is None else _operand("status", status, torch.int32, (1,), dev)
 
 
 def make_config(latent_dim, rope_dim, group, scale_fmt, idx_dim, topk, window, n_heads, sm_scale,
@@ -201,11 +209,11 @@ class Cache:
         self = cls.__new__(cls)
         self.cfg, (self.batch, self.capacity) = cfg, records.shape[:2]
         self.records, self.idx_k, self.n_entries = records, idx_k, n_entries
-        lead = (self.batch, self.capacity)
-        _operand("records", records, torch.uint8, (*lead, record_bytes(cfg)))
+        lead, dev = (self.batch, self.capacity), torch.cuda.current_device()
+        _operand("records", records, torch.uint8, (*lead, record_bytes(cfg)), dev)
         _operand("idx_k", idx_k, torch.uint8 if cfg.idx_fmt == 1 else torch.int8,
-                 (*lead, idx_row_bytes(cfg)))
-        _operand("n_entries", n_entries, torch.int32, (self.batch,))
+                 (*lead, idx_row_bytes(cfg)), dev)
+        _operand("n_entries", n_entries, torch.int32, (self.batch,), dev)
         return self
 
     def struct(self) -> CacheStruct:
@@ -323,13 +331,13 @@ def layer_group_step(cfg, modes, q, idx_q, windows, window_len, cache: Cache, ou
 def unpack(cfg, cache: Cache, rows, idx=None, first=0, status=None, stream=None):
     """Records read back: rows [B][n][D] act_dtype receives entries idx [B][n]
     int32 (-1: zeros), or entries first .. first + n - 1 without idx."""
-    n = rows.shape[1]
+    n, b = rows.shape[1], cache.batch
     d = cfg.latent_dim + cfg.rope_dim
+    dev, st = _here(stream)
     cs = cache.struct()
     _check("kvc_unpack", _lib().kvc_unpack(
-        C.byref(cfg), C.byref(cs), _operand("idx", idx, torch.int32, (cache.batch, n)), int(first),
-        n, _operand("rows", rows, _act(cfg), (cache.batch, n, d)), _status(status),
-        _stream(stream)))
+        C.byref(cfg), C.byref(cs), _operand("idx", idx, torch.int32, (b, n), dev), int(first), n,
+        _operand("rows", rows, _act(cfg), (b, n, d), dev), _status(status, dev), st))
 
 
 def unpack_window_fp8(cfg, codes, scales, rows, stream=None):
@@ -337,10 +345,11 @@ def unpack_window_fp8(cfg, codes, scales, rows, stream=None):
     pack_window_fp8 writes them -> rows [..][D] act_dtype."""
     d = cfg.latent_dim + cfg.rope_dim
     lead = scales.shape
+    dev, st = _here(stream)
     _check("kvc_unpack_window_fp8", _lib().kvc_unpack_window_fp8(
-        C.byref(cfg), _operand("codes", codes, torch.uint8, (*lead, d)),
-        _operand("scales", scales, torch.float32, lead), scales.numel(),
-        _operand("rows", rows, _act(cfg), (*lead, d)), _stream(stream)))
+        C.byref(cfg), _operand("codes", codes, torch.uint8, (*lead, d), dev),
+        _operand("scales", scales, torch.float32, lead, dev), scales.numel(),
+        _operand("rows", rows, _act(cfg), (*lead, d), dev), st))
 
 
 def norm_rope(cfg, q, k, positions, inv_freq, q_out, k_out, q_gain=None, k_gain=None,
@@ -349,32 +358,38 @@ def norm_rope(cfg, q, k, positions, inv_freq, q_out, k_out, q_gain=None, k_gain=
     """Norms and position rotation of query rows q [n][H][D] and key rows k
     [n][D] (either may be None, with its output); their first dimension may be
     strided (a slice of a wider projection), the outputs are contiguous."""
-    n, h, d = positions.shape[0], cfg.n_heads, cfg.latent_dim + cfg.rope_dim
-    act = _act(cfg)
-    width = (0, cfg.latent_dim, d)
+    n, h, lat = positions.shape[0], cfg.n_heads, cfg.latent_dim
+    d = lat + cfg.rope_dim
+    act, f32 = _act(cfg), torch.float32
+    width = (0, lat, d)
+    dev, st = _here(stream)
     qs = ks = 0
     if q is not None:
-        qs = q.stride(0) if n > 1 else h * d
-        if q.stride(2) != 1 or (h > 1 and q.stride(1) != d):
+        qs, qh, qd = q.stride()
+        if qd != 1 or (h > 1 and qh != d):
             raise ValueError("q: the heads of a token must be contiguous")
+        if n <= 1:
+            qs = h * d
         if q_out is None:
             raise ValueError("q_out: needed with q")
     if k is not None:
-        ks = k.stride(0) if n > 1 else d
-        if k.stride(1) != 1:
+        ks, kd = k.stride()
+        if kd != 1:
             raise ValueError("k: the channels of a row must be contiguous")
+        if n <= 1:
+            ks = d
         if k_out is None:
             raise ValueError("k_out: needed with k")
     _check("kvc_norm_rope", _lib().kvc_norm_rope(
-        C.byref(cfg), n, _operand("q", q, act, (n, h, d), False), qs,
-        _operand("q_gain", q_gain, torch.float32, (width[q_norm],)), q_norm,
-        _operand("q_out", q_out, act, (n, h, d)) if q is not None else None,
-        _operand("k", k, act, (n, d), False), ks,
-        _operand("k_gain", k_gain, torch.float32, (width[k_norm],)), k_norm,
-        _operand("k_out", k_out, act, (n, d)) if k is not None else None,
-        _operand("positions", positions, torch.int32, (n,)),
-        _operand("inv_freq", inv_freq, torch.float32, (cfg.rope_dim // 2,)), float(eps), layout,
-        _status(status), _stream(stream)))
+        C.byref(cfg), n, _operand("q", q, act, (n, h, d), dev, False), qs,
+        _operand("q_gain", q_gain, f32, (width[q_norm],), dev), q_norm,
+        _operand("q_out", q_out, act, (n, h, d), dev) if q is not None else None,
+        _operand("k", k, act, (n, d), dev, False), ks,
+        _operand("k_gain", k_gain, f32, (width[k_norm],), dev), k_norm,
+        _operand("k_out", k_out, act, (n, d), dev) if k is not None else None,
+        _operand("positions", positions, torch.int32, (n,), dev),
+        _operand("inv_freq", inv_freq, f32, (cfg.rope_dim // 2,), dev), eps, layout,
+        _status(status, dev), st))
 
 
 def tree_decode_attn(cfg, q, cache: Cache, topk, window, window_len, draft, parents, out, lse=None,
@@ -383,18 +398,20 @@ def tree_decode_attn(cfg, q, cache: Cache, topk, window, window_len, draft, pare
     entries and the window of its own path: q [T][B][H][D], topk [T][B][K] or
     [B][K] (one selection for all nodes), window [B][W][D], draft [T][B][D],
     parents [T][B] -> out [T][B][H][latent] act_dtype."""
-    t, b, d = q.shape[0], cache.batch, cfg.latent_dim + cfg.rope_dim
-    act, h, shared = _act(cfg), cfg.n_heads, topk.dim() == 2
+    t, b, lat = q.shape[0], cache.batch, cfg.latent_dim
+    d, h, i32 = lat + cfg.rope_dim, cfg.n_heads, torch.int32
+    act, shared = _act(cfg), topk.dim() == 2
+    dev, st = _here(stream)
     cs = cache.struct()
     _check("kvc_tree_decode_attn", _lib().kvc_tree_decode_attn(
-        C.byref(cfg), t, _operand("q", q, act, (t, b, h, d)), C.byref(cs),
-        _operand("topk", topk, torch.int32, (b, cfg.topk) if shared else (t, b, cfg.topk)),
-        int(shared), _operand("window", window, act, (b, cfg.window, d)), int(window_len),
-        _operand("window_lens", window_lens, torch.int32, (b,)),
-        _operand("draft", draft, act, (t, b, d)),
-        _operand("parents", parents, torch.int32, (t, b)),
-        _operand("out", out, act, (t, b, h, cfg.latent_dim)),
-        _operand("lse", lse, torch.float32, (t, b, h)), _status(status), _stream(stream)))
+        C.byref(cfg), t, _operand("q", q, act, (t, b, h, d), dev), C.byref(cs),
+        _operand("topk", topk, i32, (b, cfg.topk) if shared else (t, b, cfg.topk), dev), shared,
+        _operand("window", window, act, (b, cfg.window, d), dev), int(window_len),
+        _operand("window_lens", window_lens, i32, (b,), dev),
+        _operand("draft", draft, act, (t, b, d), dev),
+        _operand("parents", parents, i32, (t, b), dev),
+        _operand("out", out, act, (t, b, h, lat), dev),
+        _operand("lse", lse, torch.float32, (t, b, h), dev), _status(status, dev), st))
 
 
 def verify_tree(p, q, tokens, parents, u, v, path, n_path, next_token, status=None, stream=None):
@@ -402,25 +419,27 @@ def verify_tree(p, q, tokens, parents, u, v, path, n_path, next_token, status=No
     (fp32 or bf16; q None: greedy drafts; rows may be padded to equal steps),
     tokens, parents, u [T][B], v [B] -> path [B][T], n_path [B], next_token [B]."""
     t, b, vocab = p.shape
+    dtype, i32, f32 = p.dtype, torch.int32, torch.float32
+    dev, st = _here(stream)
 
     def rows(name, x):  # equally spaced rows t * B + b of contiguous entries
-        step = x.stride(1) if b > 1 else x.stride(0) if t > 1 else vocab
-        if (x.stride(2) != 1 and vocab > 1) or (t > 1 and b > 1 and x.stride(0) != b * step):
+        st, sb, sv = x.stride()
+        step = sb if b > 1 else st if t > 1 else vocab
+        if (sv != 1 and vocab > 1) or (t > 1 and b > 1 and st != b * step):
             raise ValueError(f"{name}: rows must be contiguous and equally spaced")
-        return _operand(name, x, p.dtype, (t, b, vocab), False), step
+        return _operand(name, x, dtype, (t, b, vocab), dev, False), step
 
-    if p.dtype not in (torch.float32, torch.bfloat16):
+    if dtype not in (f32, torch.bfloat16):
         raise ValueError("p: expected fp32 or bf16 probabilities")
     pp, ps = rows("p", p)
     qp, qs = rows("q", q) if q is not None else (None, 0)
     _check("kvc_verify_tree", _lib().kvc_verify_tree(
-        b, t, vocab, F32 if p.dtype == torch.float32 else BF16, pp, ps, qp, qs,
-        _operand("tokens", tokens, torch.int32, (t, b)),
-        _operand("parents", parents, torch.int32, (t, b)),
-        _operand("u", u, torch.float32, (t, b)), _operand("v", v, torch.float32, (b,)),
-        _operand("path", path, torch.int32, (b, t)),
-        _operand("n_path", n_path, torch.int32, (b,)),
-        _operand("next_token", next_token, torch.int32, (b,)), _status(status), _stream(stream)))
+        b, t, vocab, F32 if dtype == f32 else BF16, pp, ps, qp, qs,
+        _operand("tokens", tokens, i32, (t, b), dev),
+        _operand("parents", parents, i32, (t, b), dev), _operand("u", u, f32, (t, b), dev),
+        _operand("v", v, f32, (b,), dev), _operand("path", path, i32, (b, t), dev),
+        _operand("n_path", n_path, i32, (b,), dev),
+        _operand("next_token", next_token, i32, (b,), dev), _status(status, dev), st))
 
 
 def e2m1_encode(x, codes, stream=None):

@@ -8,11 +8,12 @@
 //
 // A record is read once (a quarter of what a bf16 row takes) and its row
 // written once: the bound is HBM, and four fifths of its bytes are writes.  A
-// thread turns 8 channels (4 code bytes) into one 16-byte store (two for
-// fp32), so a warp's stores cover 512 contiguous bytes; its products are one
-// conversion and one multiplication a channel.  Products of a code (two
-// significant bits) and a UE4M3 scale (four) are exact in bf16; with fp32
-// scales they are rounded to fp32 and then to the row's type.
+// thread keeps one place of a row, 8 channels (4 code bytes, one 16-byte store,
+// two for fp32), and goes through rows, four of them in flight: what depends on
+// the place alone (its scale's place above all) is found once, and a row's
+// places are neighbouring threads, so accesses are contiguous.  Products of a
+// code (two significant bits) and a UE4M3 scale (four) are exact in bf16; with
+// fp32 scales they are rounded to fp32 and then to the row's type.
 #include <algorithm>
 #include <cuda_fp16.h>
 
@@ -53,10 +54,12 @@ __device__ __forceinline__ void put8(float* dst, const float (&v)[8]) {
     reinterpret_cast<float4*>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Grid (tiles of rows, batch); a block takes `rows` consecutive output rows.
+// Grid (tiles of rows, batch); block of `lanes` rows' places; a tile is
+// lanes * U * rounds rows.
+constexpr int U = 4;
 template <typename T, bool UE4M3>
 __global__ void __launch_bounds__(NT)
-unpack_kernel(UnpackArgs a, Shape sh, int rows) {
+unpack_kernel(UnpackArgs a, Shape sh, int lanes, int rounds) {
     // (no early launch of dependents: kvc_pack reads its tokens before it waits
     // for the kernel in front of it, and these rows may be its tokens)
     pdl_wait();
@@ -64,29 +67,45 @@ unpack_kernel(UnpackArgs a, Shape sh, int rows) {
     const int n = a.n_entries[b];
     const bool len_ok = n >= 0 && n <= a.capacity;
     if (!len_ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(a.status, KVC_DEV_BAD_LENGTH);
-    const int j0 = blockIdx.x * rows, nj = min(rows, a.n - j0);
-    const uint8_t* base = a.records + (size_t)b * a.capacity * sh.rb;
-    T* out = static_cast<T*>(a.out) + ((size_t)b * a.n + j0) * sh.D;
-    const int lat_groups = (sh.Dv + sh.G - 1) / sh.G;
+    const int lane = threadIdx.x / np, c = threadIdx.x - lane * np;
     const int lg = 31 - __clz(sh.lpg);  // 8-channel pieces of a group: a power of two
-    for (int p = threadIdx.x; p < nj * np; p += NT) {
-        const int j = p / np, c = p - j * np;
-        int e = a.idx ? __ldg(a.idx + (size_t)b * a.n + j0 + j) : a.first + j0 + j;
-        if (e < 0 || e >= n || !len_ok) {
-            if (a.idx && e != -1 && len_ok && c == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
-            e = -1;
+    const int g = c < np_lat ? c >> lg : (sh.Dv + sh.G - 1) / sh.G + ((c - np_lat) >> lg);
+    const uint8_t* base = a.records + (size_t)b * a.capacity * sh.rb;
+    const int scale_at = sh.code_bytes + g * (UE4M3 ? 1 : 4);
+    T* out = static_cast<T*>(a.out) + (size_t)b * a.n * sh.D + 8 * c;
+    const int32_t* idx = a.idx ? a.idx + (size_t)b * a.n : nullptr;
+    int j = blockIdx.x * (lanes * U * rounds) + lane;
+    for (int round = 0; round < rounds; ++round, j += lanes * U) {
+        uint32_t codes[U];
+        float scale[U];
+        int e[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = j + lanes * u;
+            e[u] = -1;
+            if (row < a.n) e[u] = idx ? __ldg(idx + row) : a.first + row;
         }
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (e >= 0) {
-            const uint8_t* rec = base + (size_t)e * sh.rb;
-            const uint32_t codes = __ldg(reinterpret_cast<const uint32_t*>(rec) + c);
-            const int g = c < np_lat ? c >> lg : lat_groups + ((c - np_lat) >> lg);
-            const float scale =
-                UE4M3 ? e4m3_to_f32(__ldg(rec + sh.code_bytes + g))
-                      : __ldg(reinterpret_cast<const float*>(rec + sh.code_bytes) + g);
-            e2m1x8_values(codes, scale, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            codes[u] = 0u;
+            scale[u] = 0.f;
+            if (e[u] >= 0 && e[u] < n && len_ok) {
+                const uint8_t* rec = base + (size_t)e[u] * sh.rb;
+                codes[u] = __ldg(reinterpret_cast<const uint32_t*>(rec) + c);
+                scale[u] = UE4M3 ? __uint_as_float(__ldg(rec + scale_at))
+                                 : __ldg(reinterpret_cast<const float*>(rec + scale_at));
+            } else if (idx && e[u] != -1 && len_ok && c == 0) {
+                set_status(a.status, KVC_DEV_BAD_INDEX);
+            }
         }
-        put8(out + (size_t)p * 8, v);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = j + lanes * u;
+            float v[8];
+            e2m1x8_values(codes[u],
+                          UE4M3 ? e4m3_to_f32((uint8_t)__float_as_uint(scale[u])) : scale[u], v);
+            if (row < a.n) put8(out + (size_t)row * sh.D, v);
+        }
     }
 }
 
@@ -112,17 +131,24 @@ unpack_fp8_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ s
 
 cudaError_t launch_unpack(const kvc_config& c, const Shape& sh, const UnpackArgs& a,
                           cudaStream_t s) {
-    const int rows = 16;
-    const dim3 grid((a.n + rows - 1) / rows, a.batch);
+    // rows at a time: as many as a block's threads hold places for; two rounds
+    // once the grid fills the device anyway (500,000 rows of 576: 1 round 118.8
+    // us, 8 rounds 129, 32 rounds 150: short tiles keep what runs at one time
+    // close together in memory)
+    const int np = sh.D / 8, lanes = NT / np;
+    const long long tiles = (long long)a.batch * ((a.n + lanes * U - 1) / (lanes * U));
+    const int rounds = tiles >= 148 * 16 ? 2 : 1;
+    const int tile = lanes * U * rounds;
+    const dim3 grid((a.n + tile - 1) / tile, a.batch);
     const bool u = c.scale_fmt == KVC_SCALE_UE4M3;
     trace_before("unpack", s);
     cudaError_t e;
     if (c.act_dtype == KVC_BF16)
-        e = u ? launch_pdl(unpack_kernel<__nv_bfloat16, true>, grid, NT, 0, s, a, sh, rows)
-              : launch_pdl(unpack_kernel<__nv_bfloat16, false>, grid, NT, 0, s, a, sh, rows);
+        e = u ? launch_pdl(unpack_kernel<__nv_bfloat16, true>, grid, lanes * np, 0, s, a, sh, lanes, rounds)
+              : launch_pdl(unpack_kernel<__nv_bfloat16, false>, grid, lanes * np, 0, s, a, sh, lanes, rounds);
     else
-        e = u ? launch_pdl(unpack_kernel<float, true>, grid, NT, 0, s, a, sh, rows)
-              : launch_pdl(unpack_kernel<float, false>, grid, NT, 0, s, a, sh, rows);
+        e = u ? launch_pdl(unpack_kernel<float, true>, grid, lanes * np, 0, s, a, sh, lanes, rounds)
+              : launch_pdl(unpack_kernel<float, false>, grid, lanes * np, 0, s, a, sh, lanes, rounds);
     trace_after(s);
     return e;
 }

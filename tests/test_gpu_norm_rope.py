@@ -198,3 +198,19 @@ def test_refused_calls(kvc):
     wide = torch.randn(3, 8 * 80 + 4, device="cuda")
     with pytest.raises(ValueError):  # a strided output
         kvc.norm_rope(cfg, q, None, pos, freq, wide[:, :640].view(3, 8, 80), None)
+
+
+def test_longest_runs_of_a_warp(kvc):
+    """So many rows that a warp goes through several fours of them, odd counts
+    of heads and rows, in place: the same bits as in small calls."""
+    for shape, n in (((8, 8, 41, "f32"), 7501), ((64, 64, 64, "bf16"), 5003)):
+        q, k, freq, gains = _inputs(shape, n, seed=19)
+        pos = torch.arange(n, device="cuda", dtype=torch.int32)
+        cfg = _cfg(kvc, shape)
+        kw = dict(q_gain=gains[1], k_gain=gains[0])
+        want_q, want_k = torch.empty_like(q), torch.empty_like(k)
+        for i in range(0, n, 400):
+            part = slice(i, min(n, i + 400))
+            kvc.norm_rope(cfg, q[part], k[part], pos[part], freq, want_q[part], want_k[part], **kw)
+        kvc.norm_rope(cfg, q, k, pos, freq, q, k, **kw)
+        assert torch.equal(q, want_q) and torch.equal(k, want_k)

@@ -362,3 +362,86 @@ def test_refused_calls(kvc):
         bad[at] = t
         with pytest.raises(ValueError):
             kvc.tree_decode_attn(*bad, **x.kw)
+
+
+@pytest.mark.parametrize("nodes,batch", [(5, 1), (4, 4), (4, 8), (6, 8), (7, 15), (16, 11)])
+def test_splits_of_a_node(kvc, nodes, batch):
+    """Node counts for which a node's keys go to several CTAs or one, its heads
+    to one group or several, and a CTA takes one node or more."""
+    x = Case(kvc, nodes, batch, 700, seed=80 + nodes * batch)
+    assert x.call() == 0
+    x.check()
+
+
+@pytest.mark.parametrize("rising", [True, False])
+def test_references_that_move(kvc, rising):
+    """One CTA goes through all chunks of a node (more nodes than
+    multiprocessors) while the logits grow from chunk to chunk by far more than
+    a weight can, or shrink: sums and outputs so far are rescaled, again and
+    again."""
+    x = Case(kvc, 13, 12, 1024, seed=91)
+    step = np.arange(1024) * 5 // 1024  # entries from 1 to 16 times the first ones
+    scale = x.rec[:, :, 288:306]
+    scale += (8 * (step if rising else 4 - step)).astype(np.uint8)[None, :, None]
+    x.win *= 0.05
+    x.draft *= 0.05
+    x.q *= 8
+    assert x.call() == 0
+    x.check()
+
+
+def test_chunks_without_a_key(kvc):
+    """No window, and selections whose first chunks hold nothing: a head's
+    first key comes late, or never."""
+    for nodes, batch in ((3, 2), (13, 12)):
+        x = Case(kvc, nodes, batch, 700, seed=93, window=0, window_len=0)
+        x.topk[:, :, :300] = -1
+        x.topk[1, 0] = -1
+        assert x.call() == 0
+        x.check()
+        assert not x.out.t[1, 0].any()
+
+
+def test_more_nodes_than_multiprocessors(kvc):
+    """Ragged trees, lengths and windows, shared selections, several head
+    groups; a CTA takes node after node, absent ones among them."""
+    rng = np.random.default_rng(95)
+    for heads, shared in ((64, True), (48, False)):
+        parents = np.stack([np.maximum(-1, i - 1 - rng.integers(0, 4, 30)) for i in range(12)])
+        parents[np.arange(12)[:, None] >= rng.integers(0, 13, 30)] = -2
+        x = Case(kvc, 12, 30, 300, seed=96, shared=shared, heads=heads, topk=200, parents=parents,
+                 lengths=rng.integers(0, 301, 30), lens=list(rng.integers(0, 129, 30)))
+        assert x.call() == 0
+        x.check()
+
+
+def test_far_entries(kvc):
+    """Records past 4 GB of a sequence."""
+    x = Case(kvc, 3, 1, 600, seed=97)
+    cap, at = 14_000_000, 13_999_400
+    assert x.call() == 0
+    want = x.out.t.clone()
+    rb = x.rec.shape[-1]
+    records = torch.empty(1, cap, rb, dtype=torch.uint8, device="cuda")
+    records[:, at:].copy_(torch.from_numpy(x.rec))
+    idx_k = torch.empty(1, cap, 128, dtype=torch.int8, device="cuda")
+    cache = kvc.Cache.wrap(x.cfg, records, idx_k, torch.full((1,), cap, dtype=torch.int32,
+                                                            device="cuda"))
+    args = list(x.args)
+    args[2], args[3] = cache, args[3] + at
+    kvc.tree_decode_attn(*args, **x.kw)
+    assert torch.equal(x.out.t, want) and x.kw["status"].item() == 0
+
+
+def test_zero_wait_limit(kvc):
+    """Every wait gives up at once: the call returns, the status says so, the
+    next call is right."""
+    for nodes, batch in ((4, 1), (16, 11)):
+        x = Case(kvc, nodes, batch, 600, seed=98)
+        kvc.debug_set_wait_limit_ns(0)
+        try:
+            assert x.call() & kvc.DEV_TIMEOUT
+        finally:
+            kvc.debug_set_wait_limit_ns(2_000_000_000)
+        assert x.call() == 0
+        x.check()

@@ -173,3 +173,20 @@ def test_refused_calls(kvc):
     with pytest.raises(ValueError):
         kvc.unpack(cfg, cache, out.float())
     kvc.unpack(cfg, cache, out[:, :0].contiguous())  # nothing to read
+
+
+def test_long_ranges(kvc):
+    """More rows than one round of the grid: the same bits as in small calls,
+    some of them against the formula."""
+    shape = SHAPES[0]
+    cfg, cache, want = _cache(kvc, shape, 2, 30_011, seed=9)
+    out = Guarded((2, 30_011, 576), torch.bfloat16, fill=float("nan"))
+    kvc.unpack(cfg, cache, out.t)
+    out.check()
+    pick = np.r_[0:50, 15_000:15_050, 29_950:30_011]
+    _equal(out.t[:, pick], want[:, pick], shape[3], shape[4])
+    for first in range(0, 30_011, 5_000):
+        n = min(5_000, 30_011 - first)
+        part = torch.empty(2, n, 576, dtype=torch.bfloat16, device="cuda")
+        kvc.unpack(cfg, cache, part, first=first)
+        assert torch.equal(part, out.t[:, first:first + n])

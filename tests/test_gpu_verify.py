@@ -235,3 +235,30 @@ def test_refused_calls(kvc):
         kvc.verify_tree(p.transpose(0, 1), None, *args, *outs)
     with pytest.raises(ValueError):
         kvc.verify_tree(p, q, args[0].long(), *args[1:], *outs)
+
+
+@pytest.mark.parametrize("t,b,v,dtype", [(2, 160, 140_000, torch.bfloat16),
+                                         (3, 1, 1_200_003, torch.float32),
+                                         (2, 1, 4_194_304, torch.float32)])
+def test_largest_vocabularies(kvc, t, b, v, dtype):
+    """Shares of a vocabulary in blocks of more than 128 entries."""
+    p, q, tokens, parents, u, vv = _case(t, b, v, 101, dtype, star=True, noise=2.0)
+    u = np.maximum(u, np.float32(0.8))
+    *got, st = _run(kvc, p, q, tokens, parents, u, vv)
+    assert st == 0
+    _same(got, plain64.verify(_np(p), _np(q), tokens, parents, u, vv))
+
+
+def test_small_probabilities(kvc):
+    """Rows of subnormal fp32 numbers, and of single tokens next to them."""
+    v = 3000
+    g = torch.Generator(device="cuda").manual_seed(111)
+    p = torch.rand(1, 4, v, generator=g, device="cuda") * 1e-40
+    p[0, 1, 2999] = 1e-30
+    p[0, 2] = 0
+    p[0, 2, 1234] = 1.4e-45
+    vv = np.array([0.5, 0.5, 0.999, 0.0], np.float32)
+    z = np.zeros((1, 4), np.int32)
+    *got, st = _run(kvc, p, None, z, z - 1, np.zeros((1, 4), np.float32), vv)
+    assert st == 0
+    _same(got, plain64.verify(_np(p), None, z, z - 1, np.zeros((1, 4), np.float32), vv))

@@ -51,38 +51,62 @@ __device__ __forceinline__ int tree_window_len(const TreeArgs& a, int b) {
     return w;
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t m = c & 7u;  // magnitudes 0, .5, 1, 1.5, 2, 3, 4, 6
-    const float mag = m < 4u ? 0.5f * (float)m : (float)(1u << (m >> 1)) * (1.0f + 0.5f * (m & 1u)) * 0.5f;
-    return (c & 8u) ? -mag : mag;
-}
-__device__ __forceinline__ float as_f32(float v) { return v; }
-__device__ __forceinline__ float as_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ----------------------------------------------------------------------------
-// Any shape: block (8 heads, node); a warp is one head, the keys go through
-// shared memory as fp32 in chunks of 32.
+// Any shape: a block is one node and 8 heads, a warp a head.  Keys go through
+// shared memory as fp32 in chunks of 32 (rows padded by 16 bytes, so that 32
+// lanes read 16 bytes of 32 rows without a conflict): lane = key for the
+// logits, 8 sums of D / 8 products, and the chunk's softmax is one warp
+// maximum; lane = channel for the values, each key's weight by a shuffle.
+// Bound by those reads of shared memory and, for few nodes, by the chain of a
+// chunk (fp32, 8 heads of 64 + 16 channels, 64 entries and 32 tokens, cold L2:
+// 4 nodes 18.5 us, 256 nodes 20.5 us; with lane = channel for the logits too,
+// five shuffles a key, 72 and 88 us).
 constexpr int kChunk = 32;
 
-template <typename T>
+// Eight channels of a raw row.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(x[k] << 16);
+        v[2 * k + 1] = __uint_as_float(x[k] & 0xFFFF0000u);
+    }
+}
+
+template <typename T, int NI>  // NI: latent channels of a lane
 __global__ void __launch_bounds__(256)
 tree_simt_kernel(TreeArgs a, Shape sh, int H, int K, float scale_log2, int ue4m3) {
-    extern __shared__ __align__(16) float keys[];  // [kChunk][D]
-    __shared__ int kind[kChunk];                   // record, -1, or -2 - raw key
+    extern __shared__ __align__(16) float smem[];
+    __shared__ int kind[kChunk];  // record, -1, or -2 - raw key
     __shared__ int parents[kMaxTreeNodes], up[kMaxTreeNodes];
     __shared__ int s_depth, s_wl;
+    const int D = sh.D, Dv = sh.Dv, np = D >> 3, pitch = D + 4;
+    float* keys = smem;                    // [kChunk][pitch]
+    float* qs = smem + kChunk * pitch;     // [8][D]
     pdl_wait();
     const int b = blockIdx.x / a.nodes, t = blockIdx.x - b * a.nodes;
     const int node = t * a.batch + b;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int h = blockIdx.y * 8 + w;
-    const int D = sh.D, Dv = sh.Dv;
-    for (int i = threadIdx.x; i < a.nodes; i += blockDim.x)
+    for (int i = threadIdx.x; i <= t; i += blockDim.x)
         parents[i] = a.parents[(size_t)i * a.batch + b];
     const int n = a.n_entries[b];
     const bool len_ok = n >= 0 && n <= a.capacity;
+    if (h < H)
+        for (int c = lane; c < np; c += 32) {
+            float v[8];
+            load8(static_cast<const T*>(a.q) + ((size_t)node * H + h) * D + 8 * c, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qs[w * D + 8 * c + i] = v[i];
+        }
     __syncthreads();
     if (threadIdx.x == 0) {
         if (!len_ok) set_status(a.status, KVC_DEV_BAD_LENGTH);
@@ -95,19 +119,15 @@ tree_simt_kernel(TreeArgs a, Shape sh, int H, int K, float scale_log2, int ue4m3
     const int skip = wl + depth - raw;                              // older ones out of its window
     const int total = depth ? K + raw : 0;
     const int32_t* sel = a.topk_idx + (a.topk_shared ? (size_t)b : (size_t)node) * K;
+    const int np_lat = Dv >> 3, lat_groups = (Dv + sh.G - 1) / sh.G;
 
-    float q[32], o[32];
-    float m = -INFINITY, l = 0.f;
-    const T* qp = static_cast<const T*>(a.q) + ((size_t)node * H + (h < H ? h : 0)) * D;
+    float o[NI];
+    float m = -INFINITY, l = 0.f;  // l: this lane's keys
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const int d = lane + 32 * i;
-        q[i] = d < D ? as_f32(qp[d]) : 0.f;
-        o[i] = 0.f;
-    }
-    for (int c = 0; c < total; c += kChunk) {
+    for (int i = 0; i < NI; ++i) o[i] = 0.f;
+    for (int c0 = 0; c0 < total; c0 += kChunk) {
         if (threadIdx.x < kChunk) {
-            const int j = c + threadIdx.x;
+            const int j = c0 + threadIdx.x;
             int k = -1;
             if (j < K) {
                 const int idx = sel[j];
@@ -119,61 +139,73 @@ tree_simt_kernel(TreeArgs a, Shape sh, int H, int K, float scale_log2, int ue4m3
             kind[threadIdx.x] = k;
         }
         __syncthreads();
-        for (int p = threadIdx.x; p < kChunk * D; p += blockDim.x) {
-            const int s = p / D, d = p - s * D;
+        for (int p = threadIdx.x; p < kChunk * np; p += blockDim.x) {
+            const int s = p / np, c = p - s * np;
             const int k = kind[s];
-            float v = 0.f;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (k >= 0) {
                 const uint8_t* rec = a.records + ((size_t)b * a.capacity + k) * sh.rb;
-                const uint32_t code = (rec[d >> 1] >> ((d & 1) * 4)) & 15u;
-                const int g = d < Dv ? (d >> 3) / sh.lpg
-                                     : (Dv + sh.G - 1) / sh.G + ((d - Dv) >> 3) / sh.lpg;
-                const float sc = ue4m3 ? e4m3_to_f32(rec[sh.code_bytes + g])
-                                       : reinterpret_cast<const float*>(rec + sh.code_bytes)[g];
-                v = e2m1_value(code) * sc;
+                const int g = c < np_lat ? c / sh.lpg : lat_groups + (c - np_lat) / sh.lpg;
+                e2m1x8_values(__ldg(reinterpret_cast<const uint32_t*>(rec) + c),
+                              ue4m3 ? e4m3_to_f32(__ldg(rec + sh.code_bytes + g))
+                                    : __ldg(reinterpret_cast<const float*>(rec + sh.code_bytes) + g),
+                              v);
             } else if (k <= -2) {
                 const int r = -2 - k;
-                const T* row = r < wl ? static_cast<const T*>(a.window) +
-                                            ((size_t)b * a.window_stride + r) * D
-                                      : static_cast<const T*>(a.draft) +
-                                            ((size_t)up[depth - 1 - (r - wl)] * a.batch + b) * D;
-                v = as_f32(row[d]);
+                load8((r < wl ? static_cast<const T*>(a.window) + ((size_t)b * a.window_stride + r) * D
+                              : static_cast<const T*>(a.draft) +
+                                    ((size_t)up[depth - 1 - (r - wl)] * a.batch + b) * D) +
+                          8 * c,
+                      v);
             }
-            keys[p] = v;
+            float4* dst = reinterpret_cast<float4*>(keys + s * pitch + 8 * c);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
         __syncthreads();
         if (h < H) {
-            for (int s = 0; s < kChunk; ++s) {
-                if (kind[s] == -1) continue;
-                const float* kr = keys + s * D;
-                float part = 0.f;
+            float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const float4* kr = reinterpret_cast<const float4*>(keys + lane * pitch);
+            const float4* qr = reinterpret_cast<const float4*>(qs + w * D);
+#pragma unroll 2
+            for (int c = 0; c < 2 * np; c += 2) {
+                const float4 k0 = kr[c], k1 = kr[c + 1], q0 = qr[c], q1 = qr[c + 1];
+                s[0] = fmaf(q0.x, k0.x, s[0]), s[1] = fmaf(q0.y, k0.y, s[1]);
+                s[2] = fmaf(q0.z, k0.z, s[2]), s[3] = fmaf(q0.w, k0.w, s[3]);
+                s[4] = fmaf(q1.x, k1.x, s[4]), s[5] = fmaf(q1.y, k1.y, s[5]);
+                s[6] = fmaf(q1.z, k1.z, s[6]), s[7] = fmaf(q1.w, k1.w, s[7]);
+            }
+            float x = (((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]))) * scale_log2;
+            if (kind[lane] == -1) x = -INFINITY;
+            float mx = x;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+            for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float mn = fmaxf(m, mx);
+            const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
+            const float p = x == -INFINITY ? 0.f : exp2f(x - mn);
+            l = l * alpha + p;
+            m = mn;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) o[i] *= alpha;
+#pragma unroll 4
+            for (int j = 0; j < kChunk; ++j) {
+                const float pj = __shfl_sync(0xffffffffu, p, j);
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
                     const int d = lane + 32 * i;
-                    if (d < D) part = fmaf(q[i], kr[d], part);
+                    if (d < Dv) o[i] = fmaf(pj, keys[j * pitch + d], o[i]);
                 }
-#pragma unroll
-                for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-                const float x = part * scale_log2;
-                const float mn = fmaxf(m, x);
-                const float alpha = m == -INFINITY ? 0.f : exp2f(m - mn);
-                const float p = mn == -INFINITY ? 0.f : exp2f(x - mn);
-                l = l * alpha + p;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int d = lane + 32 * i;
-                    if (d < Dv) o[i] = fmaf(p, kr[d], o[i] * alpha);
-                }
-                m = mn;
             }
         }
         __syncthreads();
     }
     if (h >= H) return;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
     const float inv = l > 0.f ? 1.f / l : 0.f;
     T* op = static_cast<T*>(a.out) + ((size_t)node * H + h) * Dv;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < NI; ++i) {
         const int d = lane + 32 * i;
         if (d < Dv) put(op + d, l == 0.f ? 0.f : o[i] * inv);
     }
@@ -181,39 +213,42 @@ tree_simt_kernel(TreeArgs a, Shape sh, int H, int K, float scale_log2, int ue4m3
         a.lse[(size_t)node * H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
-cudaError_t launch_tree_simt(const kvc_config& c, const Shape& sh, const TreeArgs& a,
-                             cudaStream_t s) {
-    const size_t smem = (size_t)kChunk * sh.D * sizeof(float);
-    const bool bf = c.act_dtype == KVC_BF16;
-    static bool attr_set[64][2] = {};
+template <typename T, int NI>
+cudaError_t launch_simt(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s) {
+    const size_t smem = ((size_t)kChunk * (sh.D + 4) + 8 * sh.D) * sizeof(float);
+    static bool attr_set[64] = {};
     int dev = 0;
     cudaGetDevice(&dev);
-    if (dev >= 0 && dev < 64 && !attr_set[dev][bf]) {
-        const cudaError_t e =
-            bf ? cudaFuncSetAttribute(tree_simt_kernel<__nv_bfloat16>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kChunk * 1024 * 4)
-               : cudaFuncSetAttribute(tree_simt_kernel<float>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kChunk * 1024 * 4);
+    if (dev >= 0 && dev < 64 && !attr_set[dev]) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            tree_simt_kernel<T, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (kChunk * (1024 + 4) + 8 * 1024) * (int)sizeof(float));
         if (e != cudaSuccess) return e;
-        attr_set[dev][bf] = true;
+        attr_set[dev] = true;
     }
     const dim3 grid((unsigned)a.nodes * a.batch, (c.n_heads + 7) / 8);
-    const float scale_log2 = c.sm_scale * kLog2e;
-    const int ue4m3 = c.scale_fmt == KVC_SCALE_UE4M3;
     trace_before("tree_simt", s);
     const cudaError_t e =
-        bf ? launch_pdl(tree_simt_kernel<__nv_bfloat16>, grid, 256, smem, s, a, sh, c.n_heads,
-                        c.topk, scale_log2, ue4m3)
-           : launch_pdl(tree_simt_kernel<float>, grid, 256, smem, s, a, sh, c.n_heads, c.topk,
-                        scale_log2, ue4m3);
+        launch_pdl(tree_simt_kernel<T, NI>, grid, 256, smem, s, a, sh, c.n_heads, c.topk,
+                   c.sm_scale * kLog2e, (int)(c.scale_fmt == KVC_SCALE_UE4M3));
     trace_after(s);
     return e;
+}
+
+template <typename T>
+cudaError_t launch_simt_t(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s) {
+    if (sh.Dv <= 64) return launch_simt<T, 2>(c, sh, a, s);
+    if (sh.Dv <= 256) return launch_simt<T, 8>(c, sh, a, s);
+    if (sh.Dv <= 512) return launch_simt<T, 16>(c, sh, a, s);
+    return launch_simt<T, 32>(c, sh, a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tree(const kvc_config& c, const Shape& sh, const TreeArgs& a, cudaStream_t s) {
-    return tree_t128_supported(c, sh) ? launch_tree_t128(c, sh, a, s) : launch_tree_simt(c, sh, a, s);
+    if (tree_t128_supported(c, sh)) return launch_tree_t128(c, sh, a, s);
+    return c.act_dtype == KVC_BF16 ? launch_simt_t<__nv_bfloat16>(c, sh, a, s)
+                                   : launch_simt_t<float>(c, sh, a, s);
 }
 
 }  // namespace kvc

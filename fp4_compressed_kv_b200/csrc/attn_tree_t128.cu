@@ -480,12 +480,19 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 // and P^T; returns the largest exponent
                 auto weights = [&]() {
                     float mx = -INFINITY;
+                    float4 f[2][4];  // (the next heads' factors: P^T's stores hold loads back)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) f[0][u] = ms.sm[warp][u];
 #pragma unroll
                     for (int c8 = 0; c8 < NH / 8; ++c8) {
+                        if (c8 + 1 < NH / 8)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                f[(c8 + 1) & 1][u] = ms.sm[warp][4 * (c8 + 1) + u];
 #pragma unroll
                         for (int u = 0; u < 4; ++u) {
                             uint32_t &p0 = r[8 * c8 + 2 * u], &p1 = r[8 * c8 + 2 * u + 1];
-                            fma2(p0, p1, ms.sm[warp][4 * c8 + u]);
+                            fma2(p0, p1, f[c8 & 1][u]);
                             mx = max3(mx, __uint_as_float(p0), __uint_as_float(p1));
                             p0 = __float_as_uint(ex2(__uint_as_float(p0)));
                             p1 = __float_as_uint(ex2(__uint_as_float(p1)));
@@ -714,6 +721,10 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                         cp16(dst[k & 3] + (2 * p + (k >> 2)) * K_ATOM,
                              src[k & 3] + (2 * p + (k >> 2)) * 64, live >> (k & 3) & 1);
                     cp_commit();
+                    if (p >= 2) {  // (pairs 0 and 1 while the later ones are waited for)
+                        cp_wait<2>();
+                        filled(p - 2);
+                    }
                 }
                 if (!ok) break;
 #pragma unroll
@@ -721,10 +732,6 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     cp16(dst[k] + 8 * K_ATOM, src[k] + 512, live >> k & 1);
                 cp_commit();
                 if (!early && c == x.c0 && cr < x.c1) rec.load(recs, rb, cur, none, lane);
-                cp_wait<4>();
-                filled(0);
-                cp_wait<3>();
-                filled(1);
                 cp_wait<2>();
                 filled(2);
                 cp_wait<1>();

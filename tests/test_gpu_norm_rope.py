@@ -214,3 +214,29 @@ def test_longest_runs_of_a_warp(kvc):
             kvc.norm_rope(cfg, q[part], k[part], pos[part], freq, want_q[part], want_k[part], **kw)
         kvc.norm_rope(cfg, q, k, pos, freq, q, k, **kw)
         assert torch.equal(q, want_q) and torch.equal(k, want_k)
+
+
+def test_stream_and_graph(kvc):
+    """On another stream, and captured and replayed with other rows in place."""
+    cfg = _cfg(kvc, MLA)
+    q, k, freq, gains = _inputs(MLA, 9, seed=23)
+    pos = torch.arange(9, device="cuda", dtype=torch.int32)
+    kw = dict(q_gain=gains[1], k_gain=gains[0])
+    qo, ko, q1, k1 = (torch.empty_like(x) for x in (q, k, q, k))
+    kvc.norm_rope(cfg, q, k, pos, freq, qo, ko, **kw)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kvc.norm_rope(cfg, q, k, pos, freq, q1, k1, stream=s, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q1, qo) and torch.equal(k1, ko)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvc.norm_rope(cfg, q, k, pos, freq, q1, k1, **kw)
+    q2, k2, _, _ = _inputs(MLA, 9, seed=24)
+    q.copy_(q2)
+    k.copy_(k2)
+    pos += 77
+    graph.replay()
+    kvc.norm_rope(cfg, q2, k2, pos, freq, qo, ko, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(q1, qo) and torch.equal(k1, ko)

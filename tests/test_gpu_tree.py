@@ -445,3 +445,30 @@ def test_zero_wait_limit(kvc):
             kvc.debug_set_wait_limit_ns(2_000_000_000)
         assert x.call() == 0
         x.check()
+
+
+@pytest.mark.parametrize("shape", [MLA, TINY])
+def test_most_nodes(kvc, shape):
+    """256 nodes: a chain, siblings under it, and none."""
+    parents = np.arange(-1, 255)[:, None]
+    parents[200:240] = 150
+    parents[250:] = -2
+    x = Case(kvc, 256, 1, 100, seed=101, topk=64, parents=parents,
+             **{k: v for k, v in shape.items() if k != "topk"})
+    assert x.call() == 0
+    x.check()
+
+
+def test_most_heads_and_a_repeated_selection(kvc):
+    """256 heads in four groups; an entry selected twice counts twice."""
+    x = Case(kvc, 3, 2, 90, seed=103, heads=256, topk=48)
+    x.topk[0, 0, 1:20] = x.topk[0, 0, 0]
+    assert x.call() == 0
+    x.check()
+
+
+def test_long_windows(kvc):
+    """A window of eight chunks."""
+    x = Case(kvc, 4, 2, 60, seed=105, window=1000, window_len=1000, topk=32, lens=[1000, 333])
+    assert x.call() == 0
+    x.check()

@@ -190,3 +190,28 @@ def test_long_ranges(kvc):
         part = torch.empty(2, n, 576, dtype=torch.bfloat16, device="cuda")
         kvc.unpack(cfg, cache, part, first=first)
         assert torch.equal(part, out.t[:, first:first + n])
+
+
+def test_stream_and_graph(kvc):
+    """On another stream, and captured and replayed with other indices and
+    lengths in place."""
+    cfg, cache, want = _cache(kvc, SHAPES[0], 2, 64, seed=21)
+    idx = torch.randint(0, 64, (2, 10), device="cuda", dtype=torch.int32)
+    out = torch.empty(2, 10, 576, dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    kvc.unpack(cfg, cache, out, idx=idx, stream=s)
+    torch.cuda.synchronize()
+    _equal(out, np.stack([want[b, idx[b].cpu().numpy()] for b in range(2)]), False, "bf16")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvc.unpack(cfg, cache, out, idx=idx)
+    idx.copy_(idx.flip(1))
+    idx[0, 3] = 50
+    cache.n_entries.copy_(torch.tensor([50, 64], dtype=torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    i = idx.cpu().numpy()
+    ref = np.stack([want[b, i[b]] for b in range(2)])
+    ref[0, i[0] >= 50] = 0
+    _equal(out, ref, False, "bf16")

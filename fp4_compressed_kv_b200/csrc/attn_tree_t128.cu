@@ -18,8 +18,8 @@
 //    made inside it: its latent channels are four pairs of 64-channel atoms,
 //    and the PV products of channels 128 p ... are the only ones that read pair
 //    p.  Their commit frees it for the next chunk's values while the other
-//    products run, and the next chunk's QK starts on it as soon as it is
-//    filled.  Roles:
+//    products run, and the next chunk's QK starts on the first two pairs as
+//    soon as they are filled.  Roles:
 //      warps 0-7   softmax (thread = key, half of the heads each) and output
 //      warps 8-15  loads: the next chunk's records are in registers while
 //                  this one's are converted and stored; two groups of four
@@ -89,7 +89,7 @@ struct Item {  // what the roles know of one node
 struct Misc {
     float qs[2][64];               // softmax multiplier of the f16 queries, by item parity
     float wmax[2][2][4][32];       // chunk maxima: [parity][head half][quadrant][head]
-    alignas(16) int over[2][2][4];             // a weight passes 2^kMost: [chunk parity][head half][quadrant]
+    alignas(16) int over[2][2][4];  // a weight passes 2^kMost: [chunk parity][head half][quadrant]
     float4 sm[SOFT_WARPS][16];     // each softmax warp's multipliers and -references, two heads
     float fac[SOFT_WARPS][32];     // each softmax warp's rescale factors
     float lsum[2][4][32];          // sums of weights: [head half][quadrant][head]
@@ -97,7 +97,7 @@ struct Misc {
     short parents[kMaxTreeNodes];  // path warp's
     unsigned char up[2][kMaxTreeNodes];  // ancestors k steps up, by item parity
     Item item[2];
-    uint64_t bars[26];
+    uint64_t bars[22];
     uint32_t tmem;
     int failed;
     float ml[72 * 2];              // exchange: (m, l) of [split][head]
@@ -111,18 +111,18 @@ static_assert(SMEM_BYTES <= 232448, "shared memory of one CTA");
 enum {
     B_FULL = 0,   // [2] pairs 0 and 1, the rest of the chunk is in place (8 warps)
     B_FREE = 2,   // [3] PV products of pair 0, pair 1, all pairs are done (commit)
-    B_S = 9,      // QK done (commit)
-    B_P = 10,     // P^T is in place (8 warps)
-    B_Q = 11,     // query rows landed (TMA)
-    B_Q16 = 12,   // queries in f16 (8 warps)
-    B_MAX = 13,   // [2] chunk maxima of a head half (4 warps)
-    B_INFO = 15,  // [2] item of that parity published
-    B_ITEM = 17,  // [2] item of that parity finished by everyone (17 warps)
-    B_SUM = 19,   // [2] sums of weights of a head half (4 warps)
-    B_OVER = 21,  // [2] checks of a head half (4 warps)
-    B_REDO = 23,  // [2] P^T of a head half is in place after all (4 warps)
-    B_END = 25,
-    N_BARS = 26
+    B_S = 5,      // QK done (commit)
+    B_P = 6,      // P^T is in place (8 warps)
+    B_Q = 7,      // query rows landed (TMA)
+    B_Q16 = 8,    // queries in f16 (8 warps)
+    B_MAX = 9,    // [2] chunk maxima of a head half (4 warps)
+    B_INFO = 11,  // [2] item of that parity published
+    B_ITEM = 13,  // [2] item of that parity finished by everyone (17 warps)
+    B_SUM = 15,   // [2] sums of weights of a head half (4 warps)
+    B_OVER = 17,  // [2] checks of a head half (4 warps)
+    B_REDO = 19,  // [2] P^T of a head half is in place after all (4 warps)
+    B_END = 21,
+    N_BARS = 22
 };
 
 // A warpgroup's registers a thread.
@@ -313,9 +313,10 @@ __device__ __forceinline__ void queries_to_f16(const QueryPart& x) {
 // A load warp's part of a chunk: 32 keys, two pairs, and the RoPE channels of 16
 // keys.  Of a pair four lanes read the 64 code bytes of a record (eight keys at
 // a time, four times), so that a load touches 8 lines and not 32: the loads,
-// the stores and every barrier share one queue.  RoPE: two lanes a key.  Each item of 32 channels comes with the word of the
-// record that holds its scales; its bytes are taken out at the store (taken out
-// here, they would be waited for here).
+// the stores and every barrier share one queue.  RoPE: two lanes a key.  Each
+// item of 32 channels comes with the word of the record that holds its scales;
+// its bytes are taken out at the store (taken out here, they would be waited
+// for here).
 template <int G>
 struct Rec {
     uint4 code[2][4];

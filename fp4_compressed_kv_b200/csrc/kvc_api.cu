@@ -707,6 +707,7 @@ kvc_status kvc_unpack(const kvc_config* cfg, const kvc_cache* cache, const int32
     if (!aligned(cache->records, 16) || !aligned(cache->n_entries, 4)) return KVC_ERR_INVALID;
     if (n < 0 || (!idx && (first < 0 || (int64_t)first + n > cache->capacity)))
         return KVC_ERR_INVALID;
+    if (n > kMaxUnpackRows) return KVC_ERR_CAPACITY;
     if (n == 0 || cache->batch == 0) return KVC_OK;
     if (!rows || !aligned(rows, 16) || !aligned(idx, 4)) return KVC_ERR_INVALID;
     if (!device_ok()) return KVC_ERR_DEVICE;

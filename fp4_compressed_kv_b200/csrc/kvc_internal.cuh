@@ -208,7 +208,9 @@ struct NormRopeArgs {
 };
 cudaError_t launch_norm_rope(const kvc_config& c, const NormRopeArgs& a, cudaStream_t s);
 
-// Records read back as rows [batch][n][D] of act_dtype.
+// Records read back as rows [batch][n][D] of act_dtype.  (The kernel counts rows
+// in 32 bits, up to a tile past the last one.)
+constexpr int kMaxUnpackRows = 0x7FFF0000;
 struct UnpackArgs {
     const uint8_t* records;
     const int32_t* n_entries;

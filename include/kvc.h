@@ -288,7 +288,7 @@ kvc_status kvc_sparse_decode_attn_fp8win(const kvc_config* cfg, const void* q,
  * past n_entries[b] (silently without idx; with idx it sets
  * KVC_DEV_BAD_INDEX), every row of a sequence whose n_entries is outside
  * [0, capacity] (KVC_DEV_BAD_LENGTH).  cache->idx_k is not used and may be
- * NULL.                                                                     */
+ * NULL.  n <= 2,147,418,112 (else KVC_ERR_CAPACITY).                         */
 kvc_status kvc_unpack(const kvc_config* cfg, const kvc_cache* cache,
                       const int32_t* idx, int first, int n, void* rows,
                       uint32_t* dev_status, void* stream);

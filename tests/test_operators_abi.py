@@ -115,3 +115,10 @@ def test_without_a_device(lib):
             assert _call(fn, good, q=None, q_out=None, q_gain=None) == NO_DEVICE
         if name in ("unpack", "tree"):
             assert _call(fn, good, cache=lib.CacheStruct(A, None, A, 2, 100)) == NO_DEVICE
+
+
+def test_unpack_counts_its_rows_in_32_bits(lib):
+    """A row number and a tile behind it stay below 2^31; more rows are refused."""
+    fn, args = _calls(lib)["unpack"]
+    for n in (2**31 - 1, 2**31 - 2**16 + 1):
+        assert _call(fn, args, idx=A, n=n) == CAPACITY

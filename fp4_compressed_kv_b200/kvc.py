@@ -361,7 +361,7 @@ def norm_rope(cfg, q, k, positions, inv_freq, q_out, k_out, q_gain=None, k_gain=
     n, h, lat = positions.shape[0], cfg.n_heads, cfg.latent_dim
     d = lat + cfg.rope_dim
     act, f32 = _act(cfg), torch.float32
-    width = (0, lat, d)
+    width = {NORM_LATENT: lat, NORM_ROW: d}
     dev, st = _here(stream)
     qs = ks = 0
     if q is not None:
@@ -382,10 +382,10 @@ def norm_rope(cfg, q, k, positions, inv_freq, q_out, k_out, q_gain=None, k_gain=
             raise ValueError("k_out: needed with k")
     _check("kvc_norm_rope", _lib().kvc_norm_rope(
         C.byref(cfg), n, _operand("q", q, act, (n, h, d), dev, False), qs,
-        _operand("q_gain", q_gain, f32, (width[q_norm],), dev), q_norm,
+        _operand("q_gain", q_gain, f32, (width.get(q_norm, 0),), dev), q_norm,
         _operand("q_out", q_out, act, (n, h, d), dev) if q is not None else None,
         _operand("k", k, act, (n, d), dev, False), ks,
-        _operand("k_gain", k_gain, f32, (width[k_norm],), dev), k_norm,
+        _operand("k_gain", k_gain, f32, (width.get(k_norm, 0),), dev), k_norm,
         _operand("k_out", k_out, act, (n, d), dev) if k is not None else None,
         _operand("positions", positions, torch.int32, (n,), dev),
         _operand("inv_freq", inv_freq, f32, (cfg.rope_dim // 2,), dev), eps, layout,

@@ -122,3 +122,15 @@ def test_unpack_counts_its_rows_in_32_bits(lib):
     fn, args = _calls(lib)["unpack"]
     for n in (2**31 - 1, 2**31 - 2**16 + 1):
         assert _call(fn, args, idx=A, n=n) == CAPACITY
+
+
+def test_a_norm_without_a_name_is_refused_as_such(lib, monkeypatch):
+    """The wrapper leaves an unknown norm to the library's own check."""
+    import torch
+    cfg = lib.make_config(64, 16, 16, lib.SCALE_UE4M3, 32, 8, 16, 8, 0.1, lib.BF16)
+    monkeypatch.setattr(lib, "_here", lambda stream: (-1, 0))  # tensors of the host stand in
+    k, out = (torch.zeros(3, 80, dtype=torch.bfloat16) for _ in range(2))
+    pos, freq = torch.zeros(3, dtype=torch.int32), torch.zeros(8)
+    for norm in (3, -1):
+        with pytest.raises(lib.KvcError):
+            lib.norm_rope(cfg, None, k, pos, freq, None, out, k_norm=norm)

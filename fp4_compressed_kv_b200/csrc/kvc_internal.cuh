@@ -276,9 +276,14 @@ cudaError_t launch_fp4_codec(const float* x, int64_t n, uint8_t* out, int e4m3,
 // CTAs are scheduled while they run or drain (the selection does not: the
 // attention's clusters are placed best on SMs freed all at once);
 // each kernel does only local set-up (shared memory, tensor memory,
-// barriers, and inputs no library kernel writes) before waiting for its
-// predecessor with griddepcontrol.wait, which returns once the predecessor
-// -- and so every kernel before it -- has completed.
+// barriers) before waiting for its predecessor with griddepcontrol.wait, which
+// returns once the predecessor -- and so every kernel before it -- has
+// completed and its writes are visible.  Only that wait promises the writes: a
+// predecessor that never signals its dependents has ended when they start,
+// but need not have its stores performed.  (The one load in front of the wait
+// is the attention's queries inside a layer-group step, AttnArgs::q_ready:
+// what was launched before the step has been waited for by the step's earlier
+// kernels.)
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args... args) {

@@ -278,8 +278,6 @@ __device__ __forceinline__ void do_row(const NormRopeArgs& a, bool is_k, int tok
 template <typename T, int NPL, bool FULL>
 __global__ void __launch_bounds__(NT)
 norm_rope_kernel(NormRopeArgs a, int run) {
-    // (no early launch of dependents: kvc_pack reads its tokens before it waits
-    // for the kernel in front of it, and these rows may be its tokens)
     pdl_wait();
     const int l = threadIdx.x & 7, g = (threadIdx.x & 31) >> 3;
     const unsigned group_mask = 0xFFu << (threadIdx.x & 24);

@@ -872,6 +872,14 @@ __host__ __device__ constexpr size_t small_stage_bytes(int D) {
     return (size_t)D * (2 * sizeof(T) + sizeof(float));  // k0, k1, gate
 }
 
+// Asks for `bytes` bytes from p on into L2, a warp together; no address past
+// them is named.
+__device__ __forceinline__ void warp_prefetch_l2(const void* p, int bytes, int lane) {
+    const char* c = static_cast<const char*>(p);
+    for (int o = 128 * lane; o < bytes; o += 32 * 128)
+        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(c + o));
+}
+
 template <typename T, int MAXJ>
 __global__ void __launch_bounds__(kSmallWarps * 32)
 pack_small_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
@@ -890,10 +898,15 @@ pack_small_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
     T* s1 = s0 + D;
     float* sg = reinterpret_cast<float*>(s1 + D);
 
-    // The entry is formed before waiting for the previous kernel: the token
-    // pair, gate and indexer row are inputs no library kernel writes; only
-    // the sequence's length and the cache stores wait.  Every load in flight
-    // at once.
+    // Rows that kvc_norm_rope or kvc_unpack wrote may be the tokens, so nothing
+    // a kernel may have written is read before this wait; what will be read is
+    // asked for into L2, where later stores reach it all the same.  Every load
+    // is then in flight at once.
+    warp_prefetch_l2(k0p, 2 * D * (int)sizeof(T), lane);
+    warp_prefetch_l2(a.gate, 4 * D, lane);
+    warp_prefetch_l2(a.idx_k_new + ((long long)b * half + i) * di, di, lane);
+    pdl_wait();
+    const int base = a.n_entries[b];
     uint4 ik = make_uint4(0, 0, 0, 0);
     if (lane < (di >> 4))
         ik = __ldcs(reinterpret_cast<const uint4*>(a.idx_k_new + ((long long)b * half + i) * di) +
@@ -987,8 +1000,6 @@ pack_small_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
     }
     __syncwarp();
 
-    pdl_wait();  // the previous kernel is done: the length and the cache
-    const int base = a.n_entries[b];
     if (base < 0 || base + half > a.capacity) {
         if (i == 0 && lane == 0) set_status(a.status, KVC_DEV_CAPACITY);
         return;
@@ -1017,8 +1028,7 @@ pack_small_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
 // the xor tree over 4, 2, 1), every lane takes the weights
 // (w_t = exp(logit_t - max) / S, S summed left to right) and quantises its
 // chunks from registers: entry = fma(w0, k0, fma(w1, k1, fma(w2, k2, w3 k3))).
-// The entry is formed before the wait for the previous kernel, as in the
-// decode append; one entry per sequence also commits the new length.
+// One entry per sequence also commits the new length.
 template <typename T>
 __host__ __device__ constexpr size_t group4_stage_bytes(int D) {
     return (size_t)D * (4 * sizeof(T) + sizeof(float));  // k0..k3, gate
@@ -1040,6 +1050,12 @@ pack_group4_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
     T* st = reinterpret_cast<T*>(stage_smem + wid * group4_stage_bytes<T>(D));  // [4][D]
     float* sg = reinterpret_cast<float*>(st + 4 * D);
 
+    // before every load, as in the decode append
+    warp_prefetch_l2(kp, 4 * D * (int)sizeof(T), lane);
+    warp_prefetch_l2(a.gate, 4 * D, lane);
+    warp_prefetch_l2(a.idx_k_new + ((long long)b * per + i) * di, di, lane);
+    pdl_wait();
+    const int base = a.n_entries[b];
     uint4 ik = make_uint4(0, 0, 0, 0);
     if (lane < (di >> 4))
         ik = __ldcs(reinterpret_cast<const uint4*>(a.idx_k_new + ((long long)b * per + i) * di) +
@@ -1147,8 +1163,6 @@ pack_group4_kernel(PackArgs a, Shape sh, int ue4m3, int di) {
     }
     __syncwarp();
 
-    pdl_wait();  // the previous kernel is done: the length and the cache
-    const int base = a.n_entries[b];
     if (base < 0 || base + per > a.capacity) {
         if (i == 0 && lane == 0) set_status(a.status, KVC_DEV_CAPACITY);
         return;

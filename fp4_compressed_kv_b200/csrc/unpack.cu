@@ -43,8 +43,6 @@ constexpr int U = 4;
 template <typename T, bool UE4M3>
 __global__ void __launch_bounds__(NT)
 unpack_kernel(UnpackArgs a, Shape sh, int lanes, int rounds) {
-    // (no early launch of dependents: kvc_pack reads its tokens before it waits
-    // for the kernel in front of it, and these rows may be its tokens)
     pdl_wait();
     const int b = blockIdx.y, np = sh.D >> 3, np_lat = sh.Dv >> 3;
     const int n = a.n_entries[b];

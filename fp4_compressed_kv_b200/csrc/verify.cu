@@ -174,9 +174,10 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
         f.p = 0.f;
         f.q = 1.f;
         const bool is_child = t > 0 && f.parent >= 0 && f.parent < t;
-        if (t > 0 && !is_child && f.parent != -1 && f.parent != -2 && rank == 0)
-            set_status(a.status, KVC_DEV_BAD_INDEX);
-        if (!is_child) f.parent = -1;
+        if (!is_child && f.parent != -1) {  // no node there
+            if (f.parent != -2 && rank == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
+            f.parent = -2;
+        }
         if (is_child && (f.token < 0 || f.token >= a.vocab)) {
             if (rank == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
             f.parent = -1;
@@ -185,7 +186,6 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
             f.p = counts(as_f32(pb[row * a.p_ld + f.token]), bad);
             if (qb) f.q = counts(as_f32(qb[row * a.q_ld + f.token]), bad);
         }
-        if (t == 0) f.parent = a.parents[b] == -2 ? -2 : -1;
         facts[t] = f;
     }
     // the facts are in place, and every CTA of the cluster runs (its shared

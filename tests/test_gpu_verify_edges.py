@@ -1,0 +1,39 @@
+"""kvc_verify_tree where a tree is not there, or not as it should be."""
+import numpy as np
+import pytest
+import torch
+
+import plain64
+from test_gpu_verify import _case, _np, _run, _same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("root", [0, 3, 5, 99, -3, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("greedy", [False, True])
+def test_a_root_with_a_parent_that_is_none(kvc, root, greedy):
+    """Node 0's parent is -1, or -2 for no tree.  Anything else is flagged and
+    counts as -2, as in the attention of the same tree."""
+    p, q, tokens, parents, u, vv = _case(4, 3, 700, 11)
+    q = None if greedy else q
+    parents[0, 1] = root
+    *got, st = _run(kvc, p, q, tokens, parents, u, vv)
+    assert st == kvc.DEV_BAD_INDEX
+    parents[0, 1] = -2
+    _same(got, plain64.verify(_np(p), _np(q), tokens, parents, u, vv))
+    assert got[1][1] == 0 and got[2][1] == -1 and (got[0][1] == -1).all()
+    assert (got[1][[0, 2]] > 0).all()
+    *got, st = _run(kvc, p, q, tokens, parents, u, vv)  # and no tree at all is no error
+    assert st == 0 and got[1][1] == 0
+
+
+def test_the_attention_of_the_same_tree_agrees(kvc):
+    """A sequence whose root has a parent that is none: absent in both calls."""
+    from test_gpu_tree import Case
+    parents = np.array([[-1, 0], [0, 0], [1, 1]])
+    x = Case(kvc, 3, 2, 200, seed=3, parents=parents)
+    assert x.call() == kvc.DEV_BAD_INDEX
+    assert not x.out.t[:, 1].any() and bool((x.lse.t[:, 1] == -torch.inf).all())
+    p, q, tokens, _, u, vv = _case(3, 2, 500, 12)
+    *got, st = _run(kvc, p, q, tokens, parents.astype(np.int32), u, vv)
+    assert st == kvc.DEV_BAD_INDEX and got[1][1] == 0 and got[1][0] > 0 and got[2][1] == -1

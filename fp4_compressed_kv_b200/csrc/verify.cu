@@ -166,6 +166,9 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
     const T* qb = static_cast<const T*>(a.q);
     bool bad = false;
     pdl_wait();
+    // (without a tree the sequence's tokens and rows are not looked at: they may
+    // hold anything)
+    const bool absent = a.parents[b] != -1;
     for (int t = tid; t < a.nodes; t += NT) {
         NodeFacts f;
         f.parent = a.parents[(size_t)t * a.batch + b];
@@ -178,10 +181,10 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
             if (f.parent != -2 && rank == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
             f.parent = -2;
         }
-        if (is_child && (f.token < 0 || f.token >= a.vocab)) {
+        if (is_child && !absent && (f.token < 0 || f.token >= a.vocab)) {
             if (rank == 0) set_status(a.status, KVC_DEV_BAD_INDEX);
             f.parent = -1;
-        } else if (is_child) {
+        } else if (is_child && !absent) {
             const size_t row = (size_t)f.parent * a.batch + b;
             f.p = counts(as_f32(pb[row * a.p_ld + f.token]), bad);
             if (qb) f.q = counts(as_f32(qb[row * a.q_ld + f.token]), bad);
@@ -192,7 +195,6 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
     // memory may be written)
     asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                  "barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
-    const bool absent = facts[0].parent == -2;  // a sequence without a tree
 
     int cur = 0, n_path = 1, n_gone = 0, passes = 0;
     double S = 0.0, m = 1.0;

@@ -370,9 +370,9 @@ kvc_status kvc_tree_decode_attn(const kvc_config* cfg, int n_nodes, const void* 
  * as the target's.
  * Node 0 of every sequence is the root: a token already accepted (the last
  * one sampled).  parents as in kvc_tree_decode_attn, node 0's among them: -1,
- * or -2 where sequence b has no tree (n_path 0, next_token -1); any other
- * value sets KVC_DEV_BAD_INDEX and counts as -2.  Nodes that are not below the
- * root are never reached.
+ * or -2 where sequence b has no tree (n_path 0, next_token -1; its tokens and
+ * probabilities are not read); any other value sets KVC_DEV_BAD_INDEX and
+ * counts as -2.  Nodes that are not below the root are never reached.
  * p        row t * batch + b, p_stride elements apart (at least vocab): the
  *          target's probabilities of the token behind node t of sequence b;
  *          fp32 or bf16 (dtype, a kvc_dtype).

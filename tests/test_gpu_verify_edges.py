@@ -37,3 +37,18 @@ def test_the_attention_of_the_same_tree_agrees(kvc):
     p, q, tokens, _, u, vv = _case(3, 2, 500, 12)
     *got, st = _run(kvc, p, q, tokens, parents.astype(np.int32), u, vv)
     assert st == kvc.DEV_BAD_INDEX and got[1][1] == 0 and got[1][0] > 0 and got[2][1] == -1
+
+
+@pytest.mark.parametrize("greedy", [False, True])
+def test_a_finished_sequence_may_hold_anything(kvc, greedy):
+    """A padded batch: only the root of a finished sequence says so, its other
+    nodes, tokens and rows are what was there before.  They raise no flag."""
+    p, q, tokens, parents, u, vv = _case(5, 4, 900, 13)
+    parents[0, 2] = -2
+    tokens[1:, 2] = [-7, 900, 2 ** 31 - 1, 3]
+    p[:, 2], q[:, 2] = float("nan"), float("inf")
+    q = None if greedy else q
+    *got, st = _run(kvc, p, q, tokens, parents, u, vv)
+    assert st == 0
+    _same(got, plain64.verify(_np(p), _np(q), tokens, parents, u, vv))
+    assert got[1][2] == 0 and got[2][2] == -1

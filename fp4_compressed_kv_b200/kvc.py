@@ -146,6 +146,21 @@ def _operand(name, t, dtype, shape, dev, contiguous=True):
     raise ValueError(f"{name}: expected a contiguous tensor")
 
 
+def _records(cfg, cache, dev):
+    """The C view of `cache`, checked: the kernels step through its records by
+    the record size of the call's `cfg`, so they must be laid out as that says,
+    and live, with the lengths, on the current device `dev`."""
+    rb = record_bytes(cfg)
+    if rb:  # (0: no valid configuration, which the library says)
+        own = cache.cfg
+        if own is not cfg and (own.latent_dim != cfg.latent_dim or own.rope_dim != cfg.rope_dim or
+                               own.group != cfg.group or own.scale_fmt != cfg.scale_fmt):
+            raise ValueError("cache: its records are laid out for another configuration")
+        _operand("cache.records", cache.records, torch.uint8, (cache.batch, cache.capacity, rb), dev)
+        _operand("cache.n_entries", cache.n_entries, torch.int32, (cache.batch,), dev)
+    return cache.struct()
+
+
 def _act(cfg: Config):
     return torch.bfloat16 if cfg.act_dtype == BF16 else torch.float32
 
@@ -334,7 +349,7 @@ def unpack(cfg, cache: Cache, rows, idx=None, first=0, status=None, stream=None)
     n, b = rows.shape[1], cache.batch
     d = cfg.latent_dim + cfg.rope_dim
     dev, st = _here(stream)
-    cs = cache.struct()
+    cs = _records(cfg, cache, dev)
     _check("kvc_unpack", _lib().kvc_unpack(
         C.byref(cfg), C.byref(cs), _operand("idx", idx, torch.int32, (b, n), dev), int(first), n,
         _operand("rows", rows, _act(cfg), (b, n, d), dev), _status(status, dev), st))
@@ -402,7 +417,7 @@ def tree_decode_attn(cfg, q, cache: Cache, topk, window, window_len, draft, pare
     d, h, i32 = lat + cfg.rope_dim, cfg.n_heads, torch.int32
     act, shared = _act(cfg), topk.dim() == 2
     dev, st = _here(stream)
-    cs = cache.struct()
+    cs = _records(cfg, cache, dev)
     _check("kvc_tree_decode_attn", _lib().kvc_tree_decode_attn(
         C.byref(cfg), t, _operand("q", q, act, (t, b, h, d), dev), C.byref(cs),
         _operand("topk", topk, i32, (b, cfg.topk) if shared else (t, b, cfg.topk), dev), shared,

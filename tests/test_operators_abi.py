@@ -134,3 +134,75 @@ def test_a_norm_without_a_name_is_refused_as_such(lib, monkeypatch):
     for norm in (3, -1):
         with pytest.raises(lib.KvcError):
             lib.norm_rope(cfg, None, k, pos, freq, None, out, k_norm=norm)
+
+
+def test_a_cache_of_another_layout_or_device_is_refused(lib, monkeypatch):
+    """The kernels step through the records by the call's record size: a cache
+    whose records another configuration laid out, or whose buffers are not on
+    the current device, does not reach the library."""
+    import torch
+
+    class Reached(Exception):
+        pass
+
+    class Stub:  # the library, but nothing of it that would launch
+        kvc_record_bytes = lib.lib().kvc_record_bytes
+        kvc_idx_row_bytes = lib.lib().kvc_idx_row_bytes
+
+        def __getattr__(self, name):
+            def call(*args):
+                raise Reached
+            return call
+
+    def config(group=32, fmt=lib.SCALE_UE4M3, latent=64, rope=16, heads=8):
+        return lib.make_config(latent, rope, group, fmt, 32, 8, 16, heads, 0.1, lib.F32)
+
+    here = [-1]  # tensors of the host stand in
+    stub = Stub()
+    monkeypatch.setattr(lib, "_here", lambda stream: (here[0], 0))
+    monkeypatch.setattr(lib, "_lib", lambda: stub)
+    cfg = config()
+    i32 = dict(dtype=torch.int32)
+    rows, q = torch.zeros(2, 5, 80), torch.zeros(3, 2, 8, 80)
+    topk, win, draft = torch.zeros(3, 2, 8, **i32), torch.zeros(2, 16, 80), torch.zeros(3, 2, 80)
+    par, out = torch.zeros(3, 2, **i32), torch.zeros(3, 2, 8, 64)
+
+    def calls(c, cache):
+        return (lambda: lib.unpack(c, cache, rows),
+                lambda: lib.tree_decode_attn(c, q, cache, topk, win, 16, draft, par, out))
+
+    good = lib.Cache(cfg, 2, 20, device="cpu")
+    for call in calls(cfg, good) + calls(config(heads=8), good):
+        with pytest.raises(Reached):
+            call()
+    # a longer record, a shorter one, and one of the same size that means something else
+    others = [config(group=8), config(group=64, fmt=lib.SCALE_F32), config(group=16),
+              config(latent=48, rope=32, group=16)]
+    assert lib.record_bytes(others[2]) == lib.record_bytes(cfg) != lib.record_bytes(others[0])
+    for other in others:
+        for call in calls(cfg, lib.Cache(other, 2, 20, device="cpu")):
+            with pytest.raises(ValueError):
+                call()
+    # a configuration changed behind its cache, and buffers changed behind it
+    changed = config()
+    cache = lib.Cache(changed, 2, 20, device="cpu")
+    changed.scale_fmt = lib.SCALE_F32
+    for call in calls(changed, cache):
+        with pytest.raises(ValueError):
+            call()
+    for name, t in (("records", good.records[:1]), ("records", good.records[:, ::2]),
+                    ("n_entries", good.n_entries.long()), ("n_entries", good.n_entries[:1])):
+        cache = lib.Cache(cfg, 2, 20, device="cpu")
+        setattr(cache, name, t)
+        for call in calls(cfg, cache):
+            with pytest.raises(ValueError):
+                call()
+    # buffers on another device than the current one
+    here[0] = 0
+    with pytest.raises(ValueError):
+        lib.unpack(cfg, good, rows)
+    # an invalid configuration is left to the library's own check
+    here[0] = -1
+    for call in calls(config(group=48), good):
+        with pytest.raises(Reached):
+            call()

@@ -209,7 +209,8 @@ __device__ __forceinline__ void do_row(const NormRopeArgs& a, bool is_k, int tok
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) ss += __shfl_xor_sync(group_mask, ss, o);
         inv = 1.0f / sqrtf(ss / (float)width + a.eps);
-        if (l == 0 && live && !(ss < INFINITY)) set_status(a.status, KVC_DEV_NONFINITE);
+        if (l == 0 && live && !(ss < INFINITY && inv < INFINITY))
+            set_status(a.status, KVC_DEV_NONFINITE);
     }
     if (!live) return;
     const float2 inv2 = make_float2(inv, inv);

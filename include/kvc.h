@@ -317,9 +317,11 @@ kvc_status kvc_unpack_window_fp8(const kvc_config* cfg, const uint8_t* codes,
  *      (KVC_ROPE_HALVES) or (2i, 2i + 1) (KVC_ROPE_PAIRS).  The angle is
  *      formed and reduced in fp64, so far positions keep their precision.
  * Sums and products are fp32, rounded once to act_dtype.  Row starts 16-byte
- * aligned (base pointers and strides).  A row whose sum of squares is not
- * finite in fp32 sets KVC_DEV_NONFINITE (its output is what the formula
- * gives).  In place (q_out = q, k_out = k) where the stride is the contiguous
+ * aligned (base pointers and strides).  The squares are fp32 too: a row
+ * whose sum of them is not finite, or is 0 with eps 0 (zeros, or channels
+ * below 2^-75), has no factor and sets KVC_DEV_NONFINITE; its output is the
+ * row times what fp32 gives for the factor, 0 or not finite.  With eps 0 rows
+ * below 2^-63 lose precision.  In place (q_out = q, k_out = k) where the stride is the contiguous
  * one; other overlaps of inputs and outputs are not allowed.               */
 kvc_status kvc_norm_rope(const kvc_config* cfg, int n_rows, const void* q,
                          int64_t q_stride, const float* q_gain, int q_norm,

@@ -11,16 +11,20 @@
 // the masses so far: one running number, and one pass over the two rows for
 // each rejection.  Without draft probabilities a child was chosen for certain
 // (q(x) = 1): it is accepted where u m < r(x), and a rejection takes p(x) out
-// of r and m.  The next token is drawn from the residual of the last accepted
-// node: the lowest i whose running sum passes v times the whole sum.
+// of r and m, so m is 1 less the rejected probabilities and not the sum of what
+// is left (which would take a pass over the row for each rejection): rows whose
+// sum is not 1 keep that difference in m.  The next token is drawn from the
+// residual of the last accepted node: the lowest i whose running sum passes v
+// times the whole sum.
 //
-// Everything that decides (products, masses, running sums) is fp64: the
-// products of two fp32 numbers are exact and a border is moved by 10^-16 of
-// the mass, where fp32 sums of 10^5 terms would move it past whole tokens.  No
-// value is converted: an fp32 pattern moved up by 29 bits is the same number
-// times 2^-896 in fp64, subnormals and 0 included, so a pass works on residuals
-// of that scale (two shifts an entry, where a conversion takes a warp 8 clocks)
-// and scales their sum back.
+// Everything that decides is fp64: S q is rounded once, inside the multiply-add
+// of the residual, u m q twice, masses and running sums once an addition.  That
+// moves a border by 10^-16 of the mass (a sum of n terms by less than n / 2^53 of
+// it), where fp32 sums of 10^5 terms would move it past whole tokens.  No value
+// is converted: an fp32 pattern moved up by 29 bits is the same number times
+// 2^-896 in fp64, subnormals and 0 included, so a pass works on residuals of
+// that scale (two shifts an entry, where a conversion takes a warp 8 clocks) and
+// scales their sum back.
 //
 // A sequence is one cluster of CTAs, each with a contiguous share of the
 // vocabulary in blocks of 128 entries (more where a share has more than 1024
@@ -198,7 +202,7 @@ verify_kernel(VerifyArgs a, int cluster, int blocks_per_cta, int nsub) {
 
     int cur = 0, n_path = 1, n_gone = 0, passes = 0;
     double S = 0.0, m = 1.0;
-    bool summed = false;  // csum and share hold the residual of `cur` at S
+    bool summed = false;  // bsum and share hold the residual of `cur` at S
     const int width = BLOCK * nsub;  // entries of a block
     const int first_block = rank * blocks_per_cta;
     const int n_blocks = min(blocks_per_cta, (a.vocab + width - 1) / width - first_block);

@@ -369,7 +369,10 @@ kvc_status kvc_tree_decode_attn(const kvc_config* cfg, int n_nodes, const void* 
 
 /* Verification of drafted trees against the target's probabilities, from
  * given random numbers; the accepted tokens and the next one are distributed
- * as the target's.
+ * as the target's, as far as the rows' sums are 1: the first mass of a row is
+ * taken as 1, and with q NULL the later ones as 1 less what was rejected, so a
+ * sum that the rows' rounding has moved off 1 (bf16) shifts acceptances by that
+ * much in proportion to the mass that is left.
  * Node 0 of every sequence is the root: a token already accepted (the last
  * one sampled).  parents as in kvc_tree_decode_attn, node 0's among them: -1,
  * or -2 where sequence b has no tree (n_path 0, next_token -1; its tokens and

@@ -112,13 +112,14 @@ unpack_fp8_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ s
 
 cudaError_t launch_unpack(const kvc_config& c, const Shape& sh, const UnpackArgs& a,
                           cudaStream_t s) {
-    // rows at a time: as many as a block's threads hold places for; two rounds
-    // once the grid fills the device anyway (500,000 rows of 576: 1 round 118.8
-    // us, 8 rounds 129, 32 rounds 150: short tiles keep what runs at one time
-    // close together in memory)
+    // rows at a time: as many as a block's threads hold places for; bf16 rows in
+    // two rounds a tile once the grid fills the device anyway (1 round, 2 rounds:
+    // 500,000 bf16 rows of 576 119.7, 113.4 us, 64,000 of them 17.6, 17.0; 200,000
+    // fp32 rows 110.2, 116.6; 8 and 32 rounds of the bf16 rows 129, 150: short tiles
+    // keep what runs at one time close together in memory)
     const int np = sh.D / 8, lanes = NT / np;
     const long long tiles = (long long)a.batch * ((a.n + lanes * U - 1) / (lanes * U));
-    const int rounds = tiles >= 148 * 16 ? 2 : 1;
+    const int rounds = c.act_dtype == KVC_BF16 && tiles >= 148 * 16 ? 2 : 1;
     const int tile = lanes * U * rounds;
     const dim3 grid((a.n + tile - 1) / tile, a.batch);
     const bool u = c.scale_fmt == KVC_SCALE_UE4M3;

@@ -150,15 +150,16 @@ def _records(cfg, cache, dev):
     """The C view of `cache`, checked: the kernels step through its records by
     the record size of the call's `cfg`, so they must be laid out as that says,
     and live, with the lengths, on the current device `dev`."""
-    rb = record_bytes(cfg)
-    if rb:  # (0: no valid configuration, which the library says)
-        own = cache.cfg
-        if own is not cfg and (own.latent_dim != cfg.latent_dim or own.rope_dim != cfg.rope_dim or
-                               own.group != cfg.group or own.scale_fmt != cfg.scale_fmt):
-            raise ValueError("cache: its records are laid out for another configuration")
-        _operand("cache.records", cache.records, torch.uint8, (cache.batch, cache.capacity, rb), dev)
-        _operand("cache.n_entries", cache.n_entries, torch.int32, (cache.batch,), dev)
-    return cache.struct()
+    rb = _lib().kvc_record_bytes(C.byref(cfg))
+    if rb == 0:  # no valid configuration, which the library says
+        return cache.struct()
+    own, b, cap = cache.cfg, cache.batch, cache.capacity
+    if own is not cfg and (own.latent_dim != cfg.latent_dim or own.rope_dim != cfg.rope_dim or
+                           own.group != cfg.group or own.scale_fmt != cfg.scale_fmt):
+        raise ValueError("cache: its records are laid out for another configuration")
+    return CacheStruct(_operand("cache.records", cache.records, torch.uint8, (b, cap, rb), dev),
+                       cache.idx_k.data_ptr(),
+                       _operand("cache.n_entries", cache.n_entries, torch.int32, (b,), dev), b, cap)
 
 
 def _act(cfg: Config):

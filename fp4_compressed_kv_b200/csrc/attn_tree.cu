@@ -60,10 +60,15 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bf
 // lanes read 16 bytes of 32 rows without a conflict): lane = key for the
 // logits, 8 sums of D / 8 products, and the chunk's softmax is one warp
 // maximum; lane = channel for the values, each key's weight by a shuffle.
-// Bound by those reads of shared memory and, for few nodes, by the chain of a
-// chunk (fp32, 8 heads of 64 + 16 channels, 64 entries and 32 tokens, cold L2:
-// 4 nodes 18.5 us, 256 nodes 20.5 us; with lane = channel for the logits too,
-// five shuffles a key, 72 and 88 us).
+// Bound by a block's chain of chunks: with 512 + 64 channels, 64 heads and 640
+// keys, 4 nodes and 16 both take 247 us (cold L2 285), 20 chunks of 12.4 us.
+// By count, about half of a chunk's 23 K clocks are its reads of shared memory (8
+// warps of 576 + 144 for the logits, 512 for the values), the rest waits between;
+// a node's 8 blocks each dequantise all of its keys.  The products alone would
+// take 19 us for 16 nodes at the fp32 rate.  Small entries (fp32, 8 heads of 64 +
+// 16 channels, 64 entries and 32 tokens): 4 nodes 9.9 us, cold 13.1; 256 nodes
+// 12.8, cold 15.8 (with lane = channel for the logits too, five shuffles a key,
+// cold and launched by itself, 72 and 88 us, where this takes 18.5 and 20.5).
 constexpr int kChunk = 32;
 
 // Eight channels of a raw row.

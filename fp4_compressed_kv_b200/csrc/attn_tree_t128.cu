@@ -38,13 +38,15 @@
 //    owner joins its heads' rows in split order.
 //
 // Bound: what one K tile serialises, at a clock that the load holds at 1.8 GHz.
-// 32 x 8 nodes of 128 + 512 keys, two nodes a CTA: 84.5 K clocks, 47 us.  A
-// record chunk takes 6.5 K of them: 1.8 softmax between QK and PV, 1.8 PV, 2.8
-// QK and the stores it waits for (a product is issued in 20 clocks and takes
-// 48, 60 with waits and commits: 4.1 K for the 68 of a chunk with nothing else
-// on the multiprocessor; each reads 6 KB of operands); a node's raw chunk takes
-// 8, its end and the next one's start 11.  The last nodes leave 40 of 148
-// multiprocessors idle.
+// 32 x 8 nodes of 128 + 512 keys, two nodes a CTA: 84.5 K clocks, 47 us (52.5
+// with a cold L2).  A record chunk takes 6.5 K of them: 1.8 softmax between QK
+// and PV, 1.8 PV, 2.8 QK and the stores it waits for (a product is issued in 20
+// clocks and takes 48, 60 with waits and commits: 4.1 K for the 68 of a chunk
+// with nothing else on the multiprocessor; each reads 6 KB of operands); a
+// node's raw chunk takes 8, its end and the next one's start 11.  The last nodes
+// leave 40 of 148 multiprocessors idle.  Every variant spills 52 to 104 bytes a
+// thread (96 registers at launch); in which role that costs time is not
+// measured.
 //
 // Every wait on an mbarrier is bounded and no other barrier is used inside
 // the roles; on expiry a role sets KVC_DEV_TIMEOUT and leaves, the others

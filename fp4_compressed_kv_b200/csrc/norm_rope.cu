@@ -21,8 +21,12 @@
 // of four pairs), so the sum is three shuffles and 512 + 64 channels fill
 // every lane.  A warp takes four consecutive rows at a time and `run` such
 // fours: heads of one token share its angles, one sine and cosine a lane.
-// Measured: a prompt of 8192 tokens of 64 + 1 rows of 576 bf16 channels in 191
-// us, 6.4 TB/s (0.98 of the measured copy rate); 4 tokens in 3.5 us.
+// Measured (in a graph of twenty calls; "cold": on twenty sets of rows, with L2
+// swept before): a prompt of 8192 tokens of 64 + 1 rows of 576 bf16 channels in
+// 190 us, cold 193, 6.4 TB/s (0.98 of the measured copy rate), 4096 of fp32 195,
+// cold 197; 4 tokens 3.6, cold 5.8.  Between them waves count: 96 registers let
+// 740 CTAs of 16 rows be resident, so 180 tokens (732 CTAs) take 6.4 us and 184
+// (748) 8.5, 256 (1,040) 10.1, cold 13.9.
 #include "kvc_internal.cuh"
 
 namespace kvc {

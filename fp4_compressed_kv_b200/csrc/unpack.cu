@@ -13,9 +13,13 @@
 // the place alone (its scale's place above all) is found once, and a row's
 // places are neighbouring threads, so accesses are contiguous.  Products of a
 // code (two significant bits) and a UE4M3 scale (four) are exact in bf16; with
-// fp32 scales they are rounded to fp32 and then to the row's type.  Measured:
-// 500,000 records of 576 channels to bf16 in 113 us, 6.4 TB/s; 85 % of the issue
-// slots are taken then.
+// fp32 scales they are rounded to fp32 and then to the row's type.  Measured (in
+// a graph of twenty calls; "cold": on twenty caches, with L2 swept before):
+// 500,000 records of 576 channels to bf16 in 113.4 us, cold 113.9, 6.4 TB/s; 85 %
+// of the issue slots are taken then.  200,000 to fp32 in 110 us, 4.7 TB/s.
+// Gathered, 32 x 512: 6.3 us, cold 7.8; 1,376 CTAs where 1,332 are resident (32 x
+// 492 in 1,312 CTAs take 5.6).  FP8 window rows, a thread 8 channels of a row:
+// 500,000 in 198 us, 4.4 TB/s (a 64-bit quotient a thread for the row's scale).
 #include <algorithm>
 
 #include "kvc_internal.cuh"

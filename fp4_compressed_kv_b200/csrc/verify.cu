@@ -34,8 +34,10 @@
 // one thread a node at the start.  Bound: the rows of the last accepted node
 // and of every node with a rejection, read from HBM once and from the caches
 // in later passes; small batches by the chain of a pass, two dependent loads
-// and a cluster barrier for each rejection.  Measured: one tree of 4 over 32,000
-// tokens 6.4 us, 32 trees of 8 over 131,072 18.5 us (fp32, with draft rows).
+// and a cluster barrier for each rejection.  Measured (fp32, with draft rows, in
+// a graph of twenty calls; "cold": on twenty sets of rows, with L2 swept
+// before): one tree of 4 over 32,000 tokens 6.8 us, cold 8.8; 32 trees of 8 over
+// 131,072 16.6 us, cold 21.6.
 #include "kvc_internal.cuh"
 
 namespace kvc {

@@ -321,8 +321,9 @@ kvc_status kvc_unpack_window_fp8(const kvc_config* cfg, const uint8_t* codes,
  * whose sum of them is not finite, or is 0 with eps 0 (zeros, or channels
  * below 2^-75), has no factor and sets KVC_DEV_NONFINITE; its output is the
  * row times what fp32 gives for the factor, 0 or not finite.  With eps 0 rows
- * below 2^-63 lose precision.  In place (q_out = q, k_out = k) where the stride is the contiguous
- * one; other overlaps of inputs and outputs are not allowed.               */
+ * below 2^-63 lose precision.  In place (q_out = q, k_out = k) where the
+ * stride is the contiguous one; other overlaps of inputs and outputs are not
+ * allowed.                                                                  */
 kvc_status kvc_norm_rope(const kvc_config* cfg, int n_rows, const void* q,
                          int64_t q_stride, const float* q_gain, int q_norm,
                          void* q_out, const void* k, int64_t k_stride,
@@ -376,7 +377,7 @@ kvc_status kvc_tree_decode_attn(const kvc_config* cfg, int n_nodes, const void* 
  * Node 0 of every sequence is the root: a token already accepted (the last
  * one sampled).  parents as in kvc_tree_decode_attn, node 0's among them: -1,
  * or -2 where sequence b has no tree (n_path 0, next_token -1; its tokens and
- * probabilities are not read); any other value sets KVC_DEV_BAD_INDEX and
+ * probabilities are not looked at); any other value sets KVC_DEV_BAD_INDEX and
  * counts as -2.  Nodes that are not below the root are never reached.
  * p        row t * batch + b, p_stride elements apart (at least vocab): the
  *          target's probabilities of the token behind node t of sequence b;

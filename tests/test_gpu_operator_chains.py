@@ -1,8 +1,8 @@
 """Calls that follow one another on a stream with nothing between them, each
 on the rows that the one before has just written: kvc_norm_rope or kvc_unpack,
-then kvc_pack.  The records must be, bit for bit, those of the same calls with
-a synchronisation after each; eager, and captured once and replayed with other
-rows in place."""
+then kvc_pack or an attention.  The results must be, bit for bit, those of the
+same calls with a synchronisation after each; eager, and captured once and
+replayed with other rows in place."""
 import pytest
 import torch
 
@@ -107,3 +107,80 @@ def test_unpack_then_pack(kvc, append):
         x.clear()
         calls()
         assert all(torch.equal(a, b) for a, b in zip(x.result(), want))
+
+
+@pytest.mark.parametrize("batch,layers", [(1, 2), (8, 4), (32, 2)])
+def test_norm_rope_then_attention(kvc, batch, layers):
+    """Queries and window rows of norm_rope taken at once by the attention of a
+    tree, of single tokens and of a layer group, whose layers ask for their
+    queries early."""
+    cap, k, w = 700, 128, 32
+    cfg = kvc.make_config(512, 64, 32, kvc.SCALE_UE4M3, 128, k, w, 64, 1 / 24, kvc.BF16)
+    g = torch.Generator(device="cuda").manual_seed(batch)
+    randn = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    cache = kvc.Cache(cfg, batch, cap)
+    cache.records[..., :288] = torch.randint(0, 256, (batch, cap, 288), generator=g, device="cuda",
+                                             dtype=torch.uint8)
+    cache.records[..., 288:306] = torch.randint(0x20, 0x30, (batch, cap, 18), generator=g,
+                                                device="cuda", dtype=torch.uint8)
+    cache.idx_k.copy_(torch.randint(-127, 128, cache.idx_k.shape, generator=g, device="cuda"))
+    cache.n_entries.fill_(cap)
+    n = layers * batch
+    raw_q, raw_w = randn(n, 64, 576), randn(n * w, 576)
+    q, win = torch.empty(layers, batch, 64, 576, device="cuda").bfloat16(), \
+        torch.empty(layers, batch, w, 576, device="cuda").bfloat16()
+    pos, wpos = (torch.arange(m, dtype=torch.int32, device="cuda") for m in (n, n * w))
+    freq = (10_000.0 ** (-torch.arange(32, device="cuda") / 32.0)).float()
+    iq = torch.randint(-127, 128, (layers, batch, 128), generator=g, device="cuda").to(torch.int8)
+    topk = torch.empty(layers, batch, k, dtype=torch.int32, device="cuda")
+    sel = torch.arange(k, dtype=torch.int32, device="cuda").expand(layers, batch, k).contiguous()
+    par = torch.arange(-1, layers - 1, dtype=torch.int32, device="cuda")[:, None].repeat(1, batch)
+    ws = kvc.workspace(cfg, batch, cap)
+    out = torch.empty(layers, batch, 64, 512, device="cuda")
+    tree = torch.empty(layers, batch, 64, 512, device="cuda").bfloat16()
+    modes = [kvc.FULL] + [kvc.REUSE] * (layers - 1)
+
+    def rows(between):
+        kvc.norm_rope(cfg, None, raw_w, wpos, freq, None, win.view(-1, 576))
+        between()
+        kvc.norm_rope(cfg, raw_q, None, pos, freq, q.view(-1, 64, 576), None)
+        between()
+
+    def group(between=lambda: None):
+        rows(between)
+        kvc.layer_group_step(cfg, modes, q, iq, win, w, cache, out, topk, ws)
+
+    def single(between=lambda: None):
+        rows(between)
+        kvc.sparse_decode_attn(cfg, q[0], cache, sel[0], win[0], w, out[0], ws)
+
+    def drafted(between=lambda: None):
+        rows(between)
+        kvc.tree_decode_attn(cfg, q, cache, sel, win[0], w, draft, par, tree)
+
+    draft = randn(layers, batch, 576)
+    for run, res in ((group, out), (single, out), (drafted, tree)):
+        graph = torch.cuda.CUDAGraph()
+        run(torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            run()
+        for _ in range(6):
+            raw_q.copy_(randn(n, 64, 576))
+            raw_w.copy_(randn(n * w, 576))
+            q.zero_()
+            win.zero_()
+            res.zero_()
+            torch.cuda.synchronize()
+            run(torch.cuda.synchronize)
+            torch.cuda.synchronize()
+            want = res.clone()
+            assert torch.isfinite(want).all() and want.any()
+            for again in (run, graph.replay):
+                q.zero_()
+                win.zero_()
+                res.zero_()
+                torch.cuda.synchronize()
+                again()
+                torch.cuda.synchronize()
+                assert torch.equal(res, want)
